@@ -113,6 +113,22 @@ typedef struct {
   const float* gamma_post;  /* [d_model] post_norm gain */
 } moe_weights_t;
 
+/* Low-rank adapters of many requests beside the two latent projections: adapter a adds
+ * scale[a] * B_a (A_a x) to a projection's output for the tokens that use it.  All adapters have one
+ * rank (pad smaller ones with zero rows of A).  rank: a multiple of 8, 8 .. 128.  A pair that a call
+ * does not use may be NULL (moe_latent_down_adapters reads down_*, moe_latent_up_adapters up_*).
+ * bf16 and latent projections only.  Weights must be finite (see moe_latent_down_adapters). */
+#define MOE_ADAPTER_MAX_RANK 128
+typedef struct {
+  int32_t n_adapters;
+  int32_t rank;
+  const void* down_a;       /* [n_adapters, rank, d_model]    bf16 */
+  const void* down_b;       /* [n_adapters, d_latent, rank]   bf16 */
+  const void* up_a;         /* [n_adapters, rank, d_latent]   bf16 */
+  const void* up_b;         /* [n_adapters, d_model, rank]    bf16 */
+  const float* scale;       /* [n_adapters] */
+} moe_adapters_t;
+
 /* Human-readable name of a status code (static storage). */
 MOE_API const char* moe_status_string(moe_status_t s);
 
@@ -308,6 +324,36 @@ MOE_API moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_w
                                             float* logits_out, int32_t* topk_idx_out,
                                             float* topk_w_out, const moe_layer_taps_t* taps,
                                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* The whole layer, as moe_layer_forward defines it, for 1 .. MOE_FEW_MAX_TOKENS tokens in one
+ * persistent kernel (and one memset of its barrier counters): single-stream decoding, or the
+ * verification of a few drafted tokens, where the launches of the batch path cost as much as the
+ * weights.  bf16 or fp32, every gate, norm and residual mode of moe_layer_forward.
+ *   - adapters (optional, bf16 with latent projections): both projections get each token's adapter,
+ *     token_adapter [T] int32 as in moe_latent_down_adapters.
+ *   - Precision: z, the expert activations and outputs, y and b stay in fp32 (the batch path rounds
+ *     each to bf16); only out is rounded.  With input_norm, u is rounded to bf16 as in the batch path.
+ *     Results are deterministic, and within the batch path's rounding of moe_layer_forward's.
+ *   - Widths are multiples of 64 (bf16) or 16 (fp32).  The activations of one stage must fit in
+ *     shared memory beside the weight ring, at most about 172 KB: T * d_model * 2 bytes and
+ *     T * 4 * max(d_latent, d_ff) bytes (bf16; fp32: T * 4 * max(d_model, d_ff)).  Otherwise, and for
+ *     T > MOE_FEW_MAX_TOKENS, MOE_ERR_UNSUPPORTED: use moe_layer_forward.
+ *   - workspace: moe_few_workspace_size bytes (host arithmetic; adapters as in the call).  Its contents
+ *     need not be initialised.  Calls that share a workspace must not overlap on the GPU.
+ *   - The kernel is launched cooperatively with one CTA on every SM of the current device; its
+ *     CTAs wait for one another (bounded, MOE_ERR_TIMEOUT), so it runs when every SM has room.  It can
+ *     be captured into a CUDA graph.
+ *   - logits_out [T, n], topk_idx_out and topk_w_out [T, k] are optional, as in moe_layer_forward.
+ *   - An adapter index outside [-1, n_adapters) latches MOE_ERR_DEVICE_CHECK; its token gets none. */
+#define MOE_FEW_MAX_TOKENS 8
+MOE_API moe_status_t moe_few_workspace_size(const moe_config_t* cfg, const moe_adapters_t* adapters,
+                                            size_t* bytes);
+MOE_API moe_status_t moe_layer_forward_few(const moe_config_t* cfg, const moe_weights_t* w,
+                                           const moe_adapters_t* adapters,
+                                           const int32_t* token_adapter, const void* u,
+                                           const void* r, void* out, float* logits_out,
+                                           int32_t* topk_idx_out, float* topk_w_out,
+                                           void* workspace, size_t workspace_bytes, void* stream);
 
 /* Bytes of device staging moe_layer_forward_host needs for this configuration: two input and two
  * output buffers of T x d_model elements, each rounded up to 256 bytes. */

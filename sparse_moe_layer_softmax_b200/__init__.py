@@ -32,7 +32,8 @@ EXPORTS = ("moe_status_string", "moe_workspace_size", "moe_route", "moe_permute"
            "moe_router_split_weights", "moe_residual_update", "moe_noisy_gate",
            "moe_noisy_gate_workspace_size", "moe_host_staging_size", "moe_layer_forward_host",
            "moe_row_sumsq_parts", "moe_gather_rows", "moe_layer_forward_taps",
-           "moe_dispatch_rows")
+           "moe_dispatch_rows", "moe_few_workspace_size", "moe_layer_forward_few")
+FEW_MAX_TOKENS = 8
 PROFILE_STAGES = ("route", "latent_down", "dispatch", "expert_gate_up", "expert_down", "combine",
                   "latent_up_resgate")
 
@@ -67,6 +68,12 @@ class Weights(ctypes.Structure):
                                                "gamma_post")]
 
 
+class Adapters(ctypes.Structure):
+    """moe_adapters_t"""
+    _fields_ = [("n_adapters", ctypes.c_int32), ("rank", ctypes.c_int32)] + \
+               [(n, ctypes.c_void_p) for n in ("down_a", "down_b", "up_a", "up_b", "scale")]
+
+
 _lib = None
 
 
@@ -80,6 +87,7 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         vp, i32, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
         cp, wp = ctypes.POINTER(Config), ctypes.POINTER(Weights)
+        ap = ctypes.POINTER(Adapters)
         L.moe_status_string.restype = ctypes.c_char_p
         L.moe_status_string.argtypes = [i32]
         sigs = {
@@ -107,6 +115,8 @@ def lib():
             "moe_profile_end": [vp, vp],
             "moe_permute_static": [cp, vp, vp, vp, vp, vp, vp, vp, vp],
             "moe_dispatch_rows": [cp, vp, vp, vp, vp, vp],
+            "moe_few_workspace_size": [cp, ap, ctypes.POINTER(sz)],
+            "moe_layer_forward_few": [cp, wp, ap, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_selftest_wait_timeout": [ctypes.c_longlong, vp, vp],
         }
         for name, args in sigs.items():
@@ -314,6 +324,70 @@ def moe_layer_forward_taps(cfg, weights: Weights, u, r, out, taps: dict, logits_
         _stream(stream)))
 
 
+def make_adapters(a: dict) -> Adapters:
+    """moe_adapters_t from a dict of CUDA tensors: scale [n] fp32 and, for the projections it is
+    used with, down_a [n, r, d_model], down_b [n, d_latent, r], up_a [n, r, d_latent],
+    up_b [n, d_model, r] (bf16).  The structure keeps the tensors alive."""
+    import torch
+    n, rank = a["scale"].numel(), None
+    if a["scale"].dtype != torch.float32 or not a["scale"].is_contiguous():
+        raise ValueError("make_adapters: scale is a contiguous fp32 tensor")
+    for name, axis in (("down_a", 1), ("down_b", 2), ("up_a", 1), ("up_b", 2)):
+        t = a.get(name)
+        if t is None:
+            continue
+        if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_contiguous() or t.shape[0] != n or \
+                rank not in (None, t.shape[axis]):
+            raise ValueError(f"make_adapters: {name} is a contiguous bf16 tensor of {n} adapters "
+                             "of one rank")
+        rank = t.shape[axis]
+    if rank is None:
+        raise ValueError("make_adapters: no adapter weights")
+    ad = Adapters(n_adapters=n, rank=rank, **{k: _ptr(a.get(k)) for k, _ in Adapters._fields_[2:]})
+    ad.tensors = dict(a)
+    return ad
+
+
+def _check_adapter_shapes(cfg, adapters, token_adapter, pairs):
+    """The tensors that ``make_adapters`` kept, and the token map, against a configuration."""
+    import torch
+    if token_adapter is None or token_adapter.dtype != torch.int32 or \
+            token_adapter.numel() != cfg.T or not token_adapter.is_contiguous():
+        raise ValueError("token_adapter: a contiguous int32 tensor with one entry per token")
+    for name, t in getattr(adapters, "tensors", {}).items():
+        if name.rsplit("_", 1)[0] not in pairs or t is None:
+            continue
+        want = {"down_a": (2, cfg.d_model), "down_b": (1, cfg.d_latent), "up_a": (2, cfg.d_latent),
+                "up_b": (1, cfg.d_model)}[name]
+        if t.shape[want[0]] != want[1]:
+            raise ValueError(f"adapters: {name} has {t.shape[want[0]]} values where the layer has "
+                             f"{want[1]}")
+
+
+def few_workspace_size(cfg: Config, adapters: Adapters | None = None) -> int:
+    n = ctypes.c_size_t()
+    _check("moe_few_workspace_size", lib().moe_few_workspace_size(
+        ctypes.byref(cfg), ctypes.byref(adapters) if adapters is not None else None,
+        ctypes.byref(n)))
+    return n.value
+
+
+def moe_layer_forward_few(cfg, weights: Weights, u, r, out, logits_out=None, topk_idx_out=None,
+                          topk_w_out=None, workspace=None, workspace_bytes=0, adapters=None,
+                          token_adapter=None, stream=None):
+    """The whole layer for at most FEW_MAX_TOKENS tokens in one kernel; ``adapters`` (from
+    ``make_adapters``) with ``token_adapter`` [T] int32 (-1: none) adapt both projections."""
+    if workspace is not None and not workspace_bytes:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    if adapters is not None:
+        _check_adapter_shapes(cfg, adapters, token_adapter, ("down", "up"))
+    _check("moe_layer_forward_few", lib().moe_layer_forward_few(
+        ctypes.byref(cfg), ctypes.byref(weights),
+        ctypes.byref(adapters) if adapters is not None else None, _ptr(token_adapter), _ptr(u),
+        _ptr(r), _ptr(out), _ptr(logits_out), _ptr(topk_idx_out), _ptr(topk_w_out),
+        _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
 def moe_get_device_status(stream=None) -> int:
     return lib().moe_get_device_status(_stream(stream))
 
@@ -346,7 +420,7 @@ class MoELayer:
     """A layer instance holding its device weights and a workspace, with a forward() that takes
     device or pinned-host inputs.  Nothing here computes: forward() is one moe_layer_forward."""
 
-    def __init__(self, cfg: Config, weights: dict):
+    def __init__(self, cfg: Config, weights: dict, adapters: dict | None = None):
         import torch
         self.cfg = cfg
         self.weights = weights
@@ -355,7 +429,9 @@ class MoELayer:
             weights = dict(weights, w_router=router_split(weights["w_router"]))
             self.weights = weights
         self._w = make_weights(weights)
+        self.adapters = make_adapters(adapters) if adapters is not None else None
         self.workspace = torch.empty(workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        self._few_workspace = None
 
     def forward(self, u, r=None, out=None, logits_out=None, topk_idx_out=None, topk_w_out=None,
                 stream=None, taps: dict | None = None):
@@ -371,6 +447,24 @@ class MoELayer:
         else:
             moe_layer_forward_taps(self.cfg, self._w, u, r, out, taps, logits_out, topk_idx_out,
                                    topk_w_out, self.workspace, stream=stream)
+        return out
+
+    def forward_few(self, u, r=None, out=None, logits_out=None, topk_idx_out=None, topk_w_out=None,
+                    token_adapter=None, stream=None):
+        """One moe_layer_forward_few: the layer for at most FEW_MAX_TOKENS tokens, with the layer's
+        adapters for the tokens of ``token_adapter`` [T] int32 (-1 or no map: none)."""
+        import torch
+        if self._few_workspace is None:
+            self._few_workspace = torch.empty(few_workspace_size(self.cfg, self.adapters),
+                                              dtype=torch.uint8, device="cuda")
+        if token_adapter is not None and self.adapters is None:
+            raise ValueError("token_adapter for a layer without adapters")
+        if out is None:
+            out = torch.empty_like(u)
+        moe_layer_forward_few(self.cfg, self._w, u, r if r is not None else u, out, logits_out,
+                              topk_idx_out, topk_w_out, self._few_workspace,
+                              adapters=self.adapters if token_adapter is not None else None,
+                              token_adapter=token_adapter, stream=stream)
         return out
 
     def forward_host(self, u_hosts, out_hosts, stream=None):

@@ -10,6 +10,7 @@
 #include <vector>
 
 #include "common.cuh"
+#include "few_tokens.cuh"
 #include "gemm_splitk.cuh"
 #include "gemm_swap_pair.cuh"
 #include "gemm_tc.cuh"
@@ -931,11 +932,114 @@ moe_status_t do_resid_update(const moe_config_t& c, const void* b, const void* r
   return last_launch();
 }
 
+// ------------------------------------------------------------------ adapters
+
+// Checks an adapter stack for the projections asked for (its pointers are looked at when T > 0).
+moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, const int32_t* which,
+                            bool down, bool up) {
+  if (!ad) return MOE_ERR_INVALID_ARG;
+  if (c.dtype != MOE_BF16 || c.d_latent == 0) return MOE_ERR_UNSUPPORTED;
+  if (ad->n_adapters <= 0 || ad->rank <= 0) return MOE_ERR_INVALID_ARG;
+  if (ad->rank % 8 || ad->rank > MOE_ADAPTER_MAX_RANK) return MOE_ERR_UNSUPPORTED;
+  if (c.T == 0) return MOE_OK;
+  if (!ad->scale || !which) return MOE_ERR_INVALID_ARG;
+  if (down && (!ad->down_a || !ad->down_b)) return MOE_ERR_INVALID_ARG;
+  if (up && (!ad->up_a || !ad->up_b)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({ad->scale, which, down ? ad->down_a : nullptr, down ? ad->down_b : nullptr,
+                    up ? ad->up_a : nullptr, up ? ad->up_b : nullptr}))
+    return MOE_ERR_ALIGNMENT;
+  return MOE_OK;
+}
+
+// ------------------------------------------------------------------ the layer for a few tokens
+
+constexpr int kFewSmem = 232448 - 4096;  // dynamic shared memory: 227 KB less the static tables
+constexpr int kFewMinStages = 3;
+
+// Shared-memory layout and workspace of moe_layer_forward_few; stages == 0: it does not fit.
+struct FewLayout {
+  size_t bar, logits, z, a, s, ss, y, v_down, v_up, b, bss, total;
+  int act_bytes, stages, smem;
+};
+FewLayout few_layout(const moe_config_t& c, int rank) {
+  FewLayout L{};
+  const size_t T = c.T, TK = T * c.top_k, E = expert_in(c), H = c.d_ff, d = c.d_model;
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  L.bar = take(kFewBarriers * 64);
+  L.logits = take(T * c.n_experts * 4);
+  L.z = take(c.d_latent > 0 ? T * E * 4 : 0);
+  L.a = take(TK * H * 4);
+  L.s = take(TK * E * 4);
+  L.ss = take(c.expert_norm ? TK * (E / 16) * 4 : 0);
+  L.y = take(c.d_latent > 0 ? T * E * 4 : 0);
+  L.v_down = take(T * rank * 4);
+  L.v_up = take(T * rank * 4);
+  L.b = take(c.post_norm ? T * d * 4 : 0);
+  L.bss = take(c.post_norm ? T * (d / 16) * 4 : 0);
+  L.total = o;
+  size_t act;
+  if (c.dtype == MOE_F32) {
+    act = T * (std::max(d, H) * 4 + 16);
+  } else {
+    act = std::max(T * (d * 2 + 64), 2 * T * (H * 2 + 64));
+    if (c.d_latent > 0) act = std::max(act, 2 * T * (E * 2 + 64));
+  }
+  act = align_up(act, 128);
+  const size_t rest = 2 * kFewRedFloats * 4 + align_up(T * rank * 4, 16);
+  if (act + rest + kFewMinStages * kFewStageBytes > static_cast<size_t>(kFewSmem)) return L;
+  L.act_bytes = static_cast<int>(act);
+  L.stages = std::min<int>(kFewMaxStages, static_cast<int>((kFewSmem - act - rest) / kFewStageBytes));
+  L.smem = static_cast<int>(act + rest) + L.stages * kFewStageBytes;
+  return L;
+}
+
+moe_status_t check_few(const moe_config_t* cfg, const moe_adapters_t* ad, FewLayout* L) {
+  moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  const moe_config_t& c = *cfg;
+  if (c.T > kFewTokens) return MOE_ERR_UNSUPPORTED;
+  const int m = c.dtype == MOE_BF16 ? 64 : 16;
+  if (c.d_model % m || c.d_ff % m) return MOE_ERR_UNSUPPORTED;
+  *L = few_layout(c, ad ? std::max(ad->rank, 0) : 0);
+  return c.T > 0 && L->stages == 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
+}
+
+template <bool kF32>
+moe_status_t launch_few(const FewParams& p, int smem, cudaStream_t st) {
+  auto kern = few_layer_kernel<kF32>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [&] {
+    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
+  });
+  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  const int sms = device_info().sms;
+  if (sms <= 0) return MOE_ERR_CUDA;
+  if (cudaMemsetAsync(p.bar, 0, kFewBarriers * 64, st) != cudaSuccess) return MOE_ERR_CUDA;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = static_cast<unsigned>(sms);
+  cfg.blockDim = kFewThreads;
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeCooperative;
+  attr[0].val.cooperative = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+    cudaGetLastError();
+    return MOE_ERR_CUDA;
+  }
+  return last_launch();
+}
+
 // Host-side checks of a whole-layer forward (nothing is launched when they fail).  T == 0 passes.
+// need: bytes of workspace the call uses.
 moe_status_t check_forward(const moe_config_t* cfg, const moe_weights_t* w, const void* u,
                            const void* r, const void* out, const float* logits_out,
                            const int32_t* topk_idx_out, const float* topk_w_out,
-                           const void* workspace, size_t workspace_bytes) {
+                           const void* workspace, size_t workspace_bytes, const size_t* need = nullptr) {
   moe_status_t s = check_cfg(cfg);
   if (s != MOE_OK) return s;
   const moe_config_t& c = *cfg;
@@ -959,8 +1063,7 @@ moe_status_t check_forward(const moe_config_t* cfg, const moe_weights_t* w, cons
                         static_cast<const void*>(w->correction_bias),
                         static_cast<const void*>(w->gamma_in),
                         static_cast<const void*>(w->gamma_post)})) return MOE_ERR_ALIGNMENT;
-  const Workspace L = layout(c);
-  if (!workspace || workspace_bytes < L.total) return MOE_ERR_WORKSPACE;
+  if (!workspace || workspace_bytes < (need ? *need : layout(c).total)) return MOE_ERR_WORKSPACE;
   return MOE_OK;
 }
 
@@ -1336,6 +1439,102 @@ moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_weights_t
   tp.t = taps;
   return layer_forward_impl(cfg, w, u, r, out, logits_out, topk_idx_out, topk_w_out, tp,
                             workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_few_workspace_size(const moe_config_t* cfg, const moe_adapters_t* adapters,
+                                    size_t* bytes) {
+  FewLayout L;
+  moe_status_t s = check_few(cfg, adapters, &L);
+  if (s != MOE_OK) return s;
+  if (adapters) {
+    moe_config_t none = *cfg;
+    none.T = 0;
+    if ((s = check_adapters(none, adapters, nullptr, true, true)) != MOE_OK) return s;
+  }
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = L.total;
+  return MOE_OK;
+}
+
+moe_status_t moe_layer_forward_few(const moe_config_t* cfg, const moe_weights_t* w,
+                                   const moe_adapters_t* adapters, const int32_t* token_adapter,
+                                   const void* u, const void* r, void* out, float* logits_out,
+                                   int32_t* topk_idx_out, float* topk_w_out, void* workspace,
+                                   size_t workspace_bytes, void* stream) {
+  FewLayout L;
+  moe_status_t s = check_few(cfg, adapters, &L);
+  if (s != MOE_OK) return s;
+  const moe_config_t& c = *cfg;
+  if (adapters && (s = check_adapters(c, adapters, token_adapter, true, true)) != MOE_OK) return s;
+  if ((s = check_forward(cfg, w, u, r, out, logits_out, topk_idx_out, topk_w_out, workspace,
+                         workspace_bytes, &L.total)) != MOE_OK)
+    return s;
+  if (c.T == 0) return MOE_OK;
+  FewParams p{};
+  p.T = c.T;
+  p.d = c.d_model;
+  p.L = c.d_latent;
+  p.E = expert_in(c);
+  p.H = c.d_ff;
+  p.n = c.n_experts;
+  p.k = c.top_k;
+  p.swiglu = c.expert_act == MOE_ACT_SWIGLU;
+  p.pre_norm = c.pre_norm;
+  p.expert_norm = c.expert_norm;
+  p.resid_mode = c.resid_mode;
+  p.gate_mode = c.gate_mode;
+  p.input_norm = c.input_norm;
+  p.post_norm = c.post_norm;
+  p.wk_seg = c.dtype == MOE_BF16 && c.router_f32 ? 3 : 1;
+  p.eps = c.eps;
+  p.eps_block = c.eps_block;
+  p.tau = c.tau;
+  p.floor_ = c.resid_floor;
+  p.routed_scale = c.routed_scale;
+  p.logit_mult = c.logit_mult;
+  p.u = u;
+  p.r = r;
+  p.w_router = w->w_router;
+  p.p_down = w->p_down;
+  p.p_up = w->p_up;
+  p.w_gu = w->w_gu;
+  p.w_down = w->w_down;
+  p.gamma_pre = w->gamma_pre;
+  p.gamma_expert = w->gamma_expert;
+  p.resid_g = w->resid_g;
+  p.logit_bias = w->logit_bias;
+  p.sel_bias = w->correction_bias;
+  p.gamma_in = w->gamma_in;
+  p.gamma_post = w->gamma_post;
+  if (adapters) {
+    p.nA = adapters->n_adapters;
+    p.rank = adapters->rank;
+    p.down_a = static_cast<const uint16_t*>(adapters->down_a);
+    p.down_b = static_cast<const uint16_t*>(adapters->down_b);
+    p.up_a = static_cast<const uint16_t*>(adapters->up_a);
+    p.up_b = static_cast<const uint16_t*>(adapters->up_b);
+    p.scale = adapters->scale;
+    p.token_adapter = token_adapter;
+  }
+  p.out = out;
+  p.logits_out = logits_out;
+  p.idx_out = topk_idx_out;
+  p.w_out = topk_w_out;
+  p.bar = at<unsigned>(workspace, L.bar);
+  p.logits = at<float>(workspace, L.logits);
+  p.z = at<float>(workspace, L.z);
+  p.a = at<float>(workspace, L.a);
+  p.s = at<float>(workspace, L.s);
+  p.ss = at<float>(workspace, L.ss);
+  p.y = at<float>(workspace, L.y);
+  p.v_down = at<float>(workspace, L.v_down);
+  p.v_up = at<float>(workspace, L.v_up);
+  p.b = at<float>(workspace, L.b);
+  p.bss = at<float>(workspace, L.bss);
+  p.stages = L.stages;
+  p.act_bytes = L.act_bytes;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  return c.dtype == MOE_F32 ? launch_few<true>(p, L.smem, st) : launch_few<false>(p, L.smem, st);
 }
 
 moe_status_t moe_residual_update(const moe_config_t* cfg, const void* b, const void* r,

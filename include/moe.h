@@ -334,7 +334,7 @@ MOE_API moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_w
  *   - Precision: z, the expert activations and outputs, y and b stay in fp32 (the batch path rounds
  *     each to bf16); only out is rounded.  With input_norm, u is rounded to bf16 as in the batch path.
  *     Results are deterministic, and within the batch path's rounding of moe_layer_forward's.
- *   - Widths are multiples of 64 (bf16) or 16 (fp32).  The activations of one stage must fit in
+ *   - Widths are multiples of 64 (bf16) or 32 (fp32).  The activations of one stage must fit in
  *     shared memory beside the weight ring, at most about 172 KB: T * d_model * 2 bytes and
  *     T * 4 * max(d_latent, d_ff) bytes (bf16; fp32: T * 4 * max(d_model, d_ff)).  Otherwise, and for
  *     T > MOE_FEW_MAX_TOKENS, MOE_ERR_UNSUPPORTED: use moe_layer_forward.

@@ -10,12 +10,13 @@
 // What bounds it: at this size the layer is a stream of weights, each read once (944 MB for one
 // token of the Muse layer, about 5.9 GB for eight), with one multiply-add per weight and token.
 // So everything is arranged around that stream never pausing:
-//   - One CTA per SM.  A producer warp walks this CTA's weight tiles of every stage of the layer in
-//     order and copies them into one shared-memory ring with bulk copies; it never waits for the
+//   - One CTA per SM.  A producer thread walks this CTA's weight tiles of every stage of the layer in
+//     order and copies them into one shared-memory ring by TMA, 16 KB a box (bulk copies of one row
+//     each, 1 KB, reached 2.9 TB/s: the copy engine takes them one by one); it never waits for the
 //     arithmetic of a stage, only for ring slots and, once, for the routing.  While the CTAs wait
 //     for one another between stages, the ring fills with the next stage's weights.
-//   - A tile is 16 weight rows; eight consumer warps split its reduction, each accumulating with
-//     m16n8k16 tensor-core products: 16 weight rows on M and the tokens on N = 8.  The stream asks for
+//   - A tile is 16 weight rows; eight warps share its reduction, each accumulating with m16n8k16
+//     tensor-core products: 16 weight rows on M and the tokens on N = 8.  The stream asks for
 //     one such instruction per SM about every 12 clocks, far below what the warp-level tensor path
 //     delivers, and operands come straight from the ring without staging accumulators in TMEM.
 //     The reduction index is permuted the same way in both operands, so that every fragment is a
@@ -36,19 +37,30 @@ namespace moe {
 
 constexpr int kFewTokens = 8;                  // tokens on the MMA's N side
 constexpr int kFewSlots = kFewTokens * kMaxTopK;
-constexpr int kFewWarps = 8;                   // consumer warps
-constexpr int kFewThreads = 32 * (kFewWarps + 1);
+constexpr int kFewMmaWarps = 8;                // warps that multiply
+constexpr int kFewEpiWarps = 4;                // warps that finish tiles
+constexpr int kFewMma = 32 * kFewMmaWarps, kFewEpi = 32 * kFewEpiWarps;
+constexpr int kFewWork = kFewMma + kFewEpi;    // threads of both groups
+constexpr int kFewThreads = kFewWork + 32;     // and the producer warp
 constexpr int kFewRows = 16;                   // weight rows per tile
-constexpr int kFewRowBytes = 1024;             // bytes of each row in one ring stage
-// Rows lie 64 bytes (mod 128) apart, so the eight 16-byte loads of a quarter-warp phase (two rows,
-// four 16-byte columns) fall into distinct banks.
-constexpr int kFewRowPitch = kFewRowBytes + 64;
-constexpr int kFewStageBytes = kFewRows * kFewRowPitch;
-constexpr int kFewMaxStages = 12;
+// A ring stage is one TMA box of 8 k-blocks x 16 rows x 128 bytes, 128-byte swizzled: the 16-byte
+// unit c of row r lies at unit c ^ (r % 8) of its 128-byte line.  (Boxes of 4 k-blocks streamed the
+// expert weights of one token at 5.6 TB/s, these at 7.0.)
+constexpr int kFewBlocks = 8;                  // k-blocks (128 bytes of a row) per stage
+constexpr int kFewStageBytes = kFewBlocks * kFewRows * 128;
+constexpr int kFewMaxStages = 8;
 constexpr int kFewMaxRank = 128;
 constexpr int kFewRedPitch = 10;               // floats per row of a partial tile (no bank conflicts)
-constexpr int kFewRedFloats = kFewWarps * kFewRows * kFewRedPitch;
-constexpr int kFewBarriers = 8;                // grid-barrier counters, 64 bytes apart
+constexpr int kFewRedFloats = kFewMmaWarps * kFewRows * kFewRedPitch;
+constexpr int kFewRedBufs = 2;
+constexpr int kFewBarriers = 9;                // grid-barrier and tile counters, 64 bytes apart
+constexpr int kFewQueue = 8;                   // tiles taken from a shared counter, in flight in a CTA
+
+// The weight matrices as 4-D tensors (128 bytes of a row, rows, halves, k-blocks): two halves for
+// SwiGLU's gate and up rows, one elsewhere.
+struct FewMaps {
+  CUtensorMap router, p_down, p_up, gate_up, w_down, ad_down, ad_up;
+};
 
 struct FewParams {
   int T, d, L, E, H, n, k;      // E: expert width (L, or d without latent projections)
@@ -72,6 +84,7 @@ struct FewParams {
   unsigned* bar;                // [kFewBarriers * 16], zeroed before the launch
   float* logits;                // [T, n] pre-activation
   float* z;                     // [T, L]
+  float* zss;                   // [T, L/16] partial sums of squares of z (pre_norm)
   float* a;                     // [T*k, H]
   float* s;                     // [T*k, E] scaled expert outputs (1 + gamma) o
   float* ss;                    // [T*k, E/16] partial sums of squares of s
@@ -80,39 +93,55 @@ struct FewParams {
   float* v_up;                  // [T, rank]
   float* b;                     // [T, d] (post_norm)
   float* bss;                   // [T, d/16] (post_norm)
-  int stages;                   // ring stages
-  int act_bytes;                // activation region of shared memory
+  int pool_bytes;               // ring and activations together
+  int stages, turns;            // ring of the dense stages (few_ring)
+  int resident;                 // 1: the expert stages keep every token's z in shared memory
 };
+
+// Ring of W multiplying warps that take chunks in turn and a multiple S of W stages, the largest that
+// fit `bytes`; 0 stages: fewer than 4 fit.
+__host__ __device__ inline void few_ring(int bytes, int* stages, int* turns) {
+  int fit = bytes / kFewStageBytes;
+  fit = fit < kFewMaxStages ? fit : kFewMaxStages;
+  *stages = *turns = 0;
+  for (int w = kFewMmaWarps; w >= 4; --w)
+    if (fit / w * w > *stages) {
+      *stages = fit / w * w;
+      *turns = w;
+    }
+}
+__host__ __device__ inline int few_row_pitch(bool f32, int K) { return f32 ? K * 4 + 16 : K * 2 + 64; }
 
 // Routing tables every CTA keeps in shared memory.
 struct FewTables {
-  int idx[kFewSlots];
+  __align__(16) int idx[kFewSlots];
   float w[kFewSlots];
   int dist;                            // distinct selected experts
+  int rows;                            // activation rows the expert stages hold
+  int stages, turns;                   // their ring
   int expert[kFewSlots];               // ascending
   int count[kFewSlots];                // slots routed to that expert (at most T)
   uint8_t slot[kFewSlots][kFewTokens]; // those slots, in token order
-  int own[256];
+  int own[kFewMmaWarps], most[kFewMmaWarps];
   // adapters: the distinct ones the tokens use, and each token's (-1: none)
   int ndist_ad;
   int ad[kFewTokens];
   int tok_ad[kFewTokens];
   float inv[kMaxTopK];
-  float red[kFewWarps][kFewTokens];
+  float red[kFewMmaWarps + kFewEpiWarps];
   float norm[kFewTokens];
   int abort_;
 };
 
 enum FewPhase : int { FEW_IN = 0, FEW_UP1 = 1, FEW_DOWN2 = 2, FEW_OUT = 3 };
 
-// One 16-row weight tile: row i < split starts at base + i * ld, row i >= split at
-// base2 + (i - split) * ld (elements); rows past `valid` repeat the last valid row.
+// One 16-row weight tile: the box at rows `row` (of half `half`) of a matrix, over a whole row.
 struct FewTile {
-  const char* base;
-  const char* base2;
-  long ld_bytes;
-  int split, valid;
-  int seg_len, segs;   // reduction: segs segments of seg_len, each against activation columns 0..
+  const CUtensorMap* map;
+  int row, half;
+  int K;               // length of a row; activation columns wrap every `wrap`
+  int wrap;
+  int valid;           // rows of this tile that count (the others are another matrix's, or zero)
   int kind;            // what the epilogue does
   int r0;              // first row (feature, expert or rank index) of the tile
   int e;               // index into the distinct experts / adapters
@@ -123,8 +152,8 @@ enum FewKind : int { FEW_ROUTER, FEW_AD_DOWN, FEW_LATENT, FEW_GATEUP, FEW_EXPERT
 template <bool kF32>
 struct FewTiles {
   const FewParams& p;
+  const FewMaps& m;
   const FewTables& tb;
-  static constexpr int kEs = kF32 ? 4 : 2;
 
   __device__ int per_expert(int phase) const {
     return phase == FEW_UP1 ? (p.swiglu ? p.H / 8 : p.H / 16) : p.E / 16;
@@ -141,10 +170,18 @@ struct FewTiles {
       default: return p.L ? lead_tiles(phase) + p.d / 16 : 0;
     }
   }
-  // This CTA's tiles: contiguous runs of the expert stages (at most a few experts per CTA), strided
-  // ones of the dense stages, so that their leading tiles start at once on as many CTAs.
-  __device__ void range(int phase, int& i, int& end, int& step) const {
+  // This CTA's tiles.  Expert stages: a contiguous run (at most a few experts per CTA) of the first
+  // 13/16 of the tiles; the others are taken one by one from a shared counter, since SMs stream at
+  // rates some 10% apart (static shares alone: the slowest CTA of one token's first expert stage ended 7 us
+  // after the mean).  With fewer than 8 tiles a CTA the counter's latency would cost more than it
+  // evens out.  Dense stages: strided, so that their leading tiles start at once on as many CTAs.
+  __device__ int fixed(int phase) const {
     const int N = total(phase);
+    if (phase != FEW_UP1 && phase != FEW_DOWN2) return N;
+    return N >= 8 * static_cast<int>(gridDim.x) ? static_cast<int>(N * 13l / 16) : N;
+  }
+  __device__ void range(int phase, int& i, int& end, int& step) const {
+    const int N = fixed(phase);
     if (phase == FEW_UP1 || phase == FEW_DOWN2) {
       i = static_cast<int>(static_cast<long>(blockIdx.x) * N / gridDim.x);
       end = static_cast<int>(static_cast<long>(blockIdx.x + 1) * N / gridDim.x);
@@ -155,94 +192,74 @@ struct FewTiles {
       step = static_cast<int>(gridDim.x);
     }
   }
-  __device__ FewTile rows(const void* w, long row0, long ld, int valid) const {
-    FewTile t;
-    t.base = static_cast<const char*>(w) + row0 * ld * kEs;
-    t.base2 = t.base;
-    t.ld_bytes = ld * kEs;
-    t.split = kFewRows;
-    t.valid = min(valid, kFewRows);
-    t.seg_len = static_cast<int>(ld);
-    t.segs = 1;
-    t.e = 0;
-    return t;
+  __device__ static FewTile tile(const CUtensorMap* map, int row, int K, int kind, int r0, int e = 0,
+                                 int valid = kFewRows, int half = 0) {
+    return FewTile{map, row, half, K, K, valid, kind, r0, e};
   }
   __device__ FewTile get(int phase, int i) const {
-    FewTile t;
     if (phase == FEW_IN) {
       const int nr = (p.n + 15) / 16, na = tb.ndist_ad * ad_tiles();
       if (i < nr) {
-        t = rows(p.w_router, i * 16l, static_cast<long>(p.wk_seg) * p.d, p.n - i * 16);
-        t.seg_len = p.d;
-        t.segs = p.wk_seg;
-        t.kind = FEW_ROUTER;
-        t.r0 = i * 16;
-      } else if (i < nr + na) {
-        const int j = i - nr, q = j / ad_tiles(), r0 = (j - q * ad_tiles()) * 16;
-        t = rows(p.down_a, static_cast<long>(tb.ad[q]) * p.rank + r0, p.d, p.rank - r0);
-        t.kind = FEW_AD_DOWN;
-        t.r0 = r0;
-        t.e = q;
-      } else {
-        t.r0 = (i - nr - na) * 16;
-        const int r0 = t.r0;
-        t = rows(p.p_down, r0, p.d, 16);
-        t.kind = FEW_LATENT;
-        t.r0 = r0;
+        FewTile t = tile(&m.router, i * 16, p.wk_seg * p.d, FEW_ROUTER, i * 16);
+        t.wrap = p.d;
+        return t;
       }
-    } else if (phase == FEW_UP1 || phase == FEW_DOWN2) {
-      const int per = per_expert(phase), q = i / per, j = i - q * per;
-      const long e = tb.expert[q];
-      if (phase == FEW_DOWN2) {
-        t = rows(p.w_down, e * p.E + j * 16, p.H, 16);
-        t.kind = FEW_EXPERT_OUT;
-        t.r0 = j * 16;
-      } else if (p.swiglu) {
-        t = rows(p.w_gu, e * 2 * p.H + j * 8, p.E, 16);
-        t.base2 = t.base + static_cast<long>(p.H) * t.ld_bytes;
-        t.split = 8;
-        t.kind = FEW_GATEUP;
-        t.r0 = j * 8;
-      } else {
-        t = rows(p.w_gu, e * p.H + j * 16, p.E, 16);
-        t.kind = FEW_GATEUP;
-        t.r0 = j * 16;
-      }
-      t.e = q;
-    } else {
-      const int na = tb.ndist_ad * ad_tiles();
-      if (i < na) {
-        const int q = i / ad_tiles(), r0 = (i - q * ad_tiles()) * 16;
-        t = rows(p.up_a, static_cast<long>(tb.ad[q]) * p.rank + r0, p.L, p.rank - r0);
-        t.kind = FEW_AD_UP;
-        t.r0 = r0;
-        t.e = q;
-      } else {
-        const int r0 = (i - na) * 16;
-        t = rows(p.p_up, r0, p.L, 16);
-        t.kind = FEW_LAYER_OUT;
-        t.r0 = r0;
-      }
+      if (i < nr + na) return ad_tile(&m.ad_down, i - nr, p.d, FEW_AD_DOWN);
+      const int r0 = (i - nr - na) * 16;
+      return tile(&m.p_down, r0, p.d, FEW_LATENT, r0);
     }
-    return t;
+    if (phase == FEW_OUT) {
+      const int na = tb.ndist_ad * ad_tiles();
+      if (i < na) return ad_tile(&m.ad_up, i, p.L, FEW_AD_UP);
+      const int r0 = (i - na) * 16;
+      return tile(&m.p_up, r0, p.L, FEW_LAYER_OUT, r0);
+    }
+    const int per = per_expert(phase), q = i / per, j = i - q * per, e = tb.expert[q];
+    if (phase == FEW_DOWN2) return tile(&m.w_down, e * p.E + j * 16, p.H, FEW_EXPERT_OUT, j * 16, q);
+    if (p.swiglu) return tile(&m.gate_up, j * 8, p.E, FEW_GATEUP, j * 8, q, kFewRows, 2 * e);
+    return tile(&m.gate_up, e * p.H + j * 16, p.E, FEW_GATEUP, j * 16, q);
+  }
+  __device__ FewTile ad_tile(const CUtensorMap* map, int i, int K, int kind) const {
+    const int q = i / ad_tiles(), r0 = (i - q * ad_tiles()) * 16;
+    return tile(map, tb.ad[q] * p.rank + r0, K, kind, r0, q, min(p.rank - r0, kFewRows));
   }
 };
 
-__device__ __forceinline__ void few_bar() {
-  asm volatile("bar.sync 1, %0;" ::"n"(32 * kFewWarps) : "memory");
+__device__ __forceinline__ void tma_load_4d(const CUtensorMap* m, uint64_t* bar, void* dst, int32_t c0,
+                                            int32_t c1, int32_t c2, int32_t c3, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
+      "l"(policy)
+      : "memory");
 }
 
-// Grid barrier b: every consumer thread calls arrive once (its earlier global writes are then
-// published), and every consumer thread calls wait before it reads what other CTAs wrote.
+// Named barriers: the multiplying and finishing warps together, and each group alone.
+enum FewBar : int { FEW_WORK = 1, FEW_MMA = 2, FEW_EPI = 3 };
+template <int kBar>
+__device__ __forceinline__ void few_bar() {
+  asm volatile("bar.sync %0, %1;" ::"n"(kBar),
+               "n"(kBar == FEW_WORK ? kFewWork : kBar == FEW_MMA ? kFewMma : kFewEpi)
+               : "memory");
+}
+template <int kBar>
+__device__ __forceinline__ bool few_first() {
+  return threadIdx.x == (kBar == FEW_EPI ? kFewMma : 0);
+}
+
+// Grid barrier b: the threads of one group arrive in every CTA (their earlier global writes are then
+// published), and a group waits before it reads what other CTAs wrote.
+template <int kBar>
 __device__ __forceinline__ void few_arrive(unsigned* bar, int b) {
-  few_bar();
-  if (threadIdx.x == 0) {
-    __threadfence();
+  few_bar<kBar>();
+  if (few_first<kBar>()) {  // the release covers what the group's threads wrote before the barrier
     asm volatile("red.release.gpu.global.add.u32 [%0], 1;" ::"l"(bar + b * 16) : "memory");
   }
 }
+template <int kBar>
 __device__ __forceinline__ void few_wait(unsigned* bar, int b, volatile int* abort_) {
-  if (threadIdx.x == 0 && !*abort_) {
+  if (few_first<kBar>() && !*abort_) {
     const long long t0 = clock64();
     unsigned v;
     for (;;) {
@@ -254,9 +271,8 @@ __device__ __forceinline__ void few_wait(unsigned* bar, int b, volatile int* abo
         break;
       }
     }
-    __threadfence();
   }
-  few_bar();
+  few_bar<kBar>();
 }
 
 __device__ __forceinline__ void few_mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -279,7 +295,7 @@ template <bool kF32>
 __device__ __forceinline__ FewAct few_act(char* base, int rows, int K, bool split) {
   FewAct a;
   a.base = base;
-  a.pitch = kF32 ? K * 4 + 16 : K * 2 + 64;
+  a.pitch = few_row_pitch(kF32, K);
   a.plane = (!kF32 && split) ? rows * a.pitch : 0;
   return a;
 }
@@ -304,46 +320,99 @@ __device__ __forceinline__ void few_act_put4(const FewAct& a, int row, int c, fl
   }
 }
 
-// One warp's share of a stage: 32-value blocks (fp32: 4-value blocks) warp, warp + 8, ... of the
-// chunk's kw columns, added into acc (m16n8 fragment: rows lane/4 and lane/4 + 8, tokens
-// 2 (lane%4) and + 1).  arow: this lane's activation row (token lane/4; fp32: unused) at the chunk's
-// first column, nullptr for a column without a token.
-__device__ __forceinline__ void few_chunk_bf16(const char* stage, int kw, const char* arow, int plane,
-                                               int warp, int lane, float (&acc)[4]) {
-  const int g = lane >> 2, t = lane & 3;
-  const char* w0 = stage + g * kFewRowPitch + t * 16;
-  float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  const uint4 zero = make_uint4(0, 0, 0, 0);
-#pragma unroll 2
-  for (int kb = warp; kb < kw / 32; kb += kFewWarps) {
-    const uint4 x = *reinterpret_cast<const uint4*>(w0 + kb * 64);
-    const uint4 y = *reinterpret_cast<const uint4*>(w0 + 8 * kFewRowPitch + kb * 64);
-    uint4 h = zero;
-    if (arow) h = *reinterpret_cast<const uint4*>(arow + kb * 64 + t * 16);
-    few_mma(d, x.x, y.x, x.y, y.y, h.x, h.y);
-    few_mma(d, x.z, y.z, x.w, y.w, h.z, h.w);
-    if (plane) {
-      uint4 l = zero;
-      if (arow) l = *reinterpret_cast<const uint4*>(arow + plane + kb * 64 + t * 16);
-      few_mma(d, x.x, y.x, x.y, y.y, l.x, l.y);
-      few_mma(d, x.z, y.z, x.w, y.w, l.z, l.w);
+// Tile row of MMA row g (and + 8 of g + 8).  The eight lanes of a shared-memory phase hold MMA rows
+// 2q and 2q + 1 and four neighbouring 16-byte units; tile rows q and q + 4 put them, after the swizzle,
+// into eight distinct units.
+__device__ __forceinline__ int few_row(int g) { return (g >> 1) + 4 * (g & 1); }
+
+// 16 bytes at a shared-memory address.  (Loads through pointers into the aligned ring would be generic
+// ones, twice the latency: the layer at eight tokens ran at 4.1 TB/s with them.)
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 lds128f(uint32_t a) {
+  const uint4 v = lds128(a);
+  return make_float4(__uint_as_float(v.x), __uint_as_float(v.y), __uint_as_float(v.z),
+                     __uint_as_float(v.w));
+}
+
+// One stage of kw columns by one warp, added into acc (m16n8 fragment: MMA rows lane/4 and
+// lane/4 + 8, columns 2 (lane%4) and + 1).  Shared-memory addresses: stage; arow, the activation row
+// of this lane's MMA column (lane/4), or 0 for an empty one; arow2, a second plane multiplied by the
+// same weights (kTwo).  col: the row's column of the stage's first value, wrapping at `wrap`.
+// With one plane, all loads of a 64-value block are issued before the products of the block before it:
+// left in program order, each 32-value step waited for its own loads (about 160 clocks a step).  Two
+// planes (an expert with more than four of the tokens; rare) have products enough to cover them, and
+// no registers for it.
+template <bool kTwo>
+__device__ __forceinline__ void few_chunk_bf16(uint32_t stage, int kw, uint32_t arow, uint32_t arow2,
+                                               int col, int wrap, int lane, float (&acc)[4]) {
+  const int t = lane & 3, r = few_row(lane >> 2);
+  // even and odd 32-value blocks lie in the two halves of a 128-byte line
+  const uint32_t w0 = stage + r * 128 + ((t ^ (r & 7)) << 4);
+  const uint32_t w1 = stage + r * 128 + (((4 + t) ^ (r & 7)) << 4);
+  float d[4][4] = {};
+  constexpr int kBufs = kTwo ? 1 : 2;
+  uint4 x[kBufs][2], y[kBufs][2], h[kBufs][2], l[kBufs][2];
+#pragma unroll
+  for (int i = 0; i < kBufs; ++i)
+#pragma unroll
+    for (int q = 0; q < 2; ++q) h[i][q] = l[i][q] = make_uint4(0, 0, 0, 0);
+  auto load = [&](int kb, int buf) {
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const uint32_t w = (q ? w1 : w0) + kb * (kFewRows * 128);
+      x[buf][q] = lds128(w);
+      y[buf][q] = lds128(w + 8 * 128);
+      if (arow) {
+        h[buf][q] = lds128(arow + t * 16 + col * 2 + q * 64);
+        if (kTwo) l[buf][q] = lds128(arow2 + t * 16 + col * 2 + q * 64);
+      }
+    }
+    col += 64;
+    if (col >= wrap) col -= wrap;
+  };
+  const int nb = kw / 64;
+  if (!kTwo) load(0, 0);
+#pragma unroll
+  for (int kb = 0; kb < kFewBlocks; ++kb) {
+    if (kb >= nb) break;
+    const int u = kTwo ? 0 : kb & 1;
+    if (kTwo) load(kb, 0);
+    else if (kb + 1 < nb) load(kb + 1, (u ^ 1) % kBufs);
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      float(&d0)[4] = d[kTwo ? 0 : 2 * q];
+      float(&d1)[4] = d[kTwo ? 1 : 2 * q + 1];
+      few_mma(d0, x[u][q].x, y[u][q].x, x[u][q].y, y[u][q].y, h[u][q].x, h[u][q].y);
+      few_mma(d1, x[u][q].z, y[u][q].z, x[u][q].w, y[u][q].w, h[u][q].z, h[u][q].w);
+      if (kTwo) {
+        few_mma(d[2], x[u][q].x, y[u][q].x, x[u][q].y, y[u][q].y, l[u][q].x, l[u][q].y);
+        few_mma(d[3], x[u][q].z, y[u][q].z, x[u][q].w, y[u][q].w, l[u][q].z, l[u][q].w);
+      }
     }
   }
-  // The chunk's short sums are added in fp32 registers: the tensor core's own accumulation
+  // The stage's short sums are added in fp32 registers: the tensor core's own accumulation
   // truncates, which over a whole row would cost the router's logits a digit.
 #pragma unroll
-  for (int i = 0; i < 4; ++i) acc[i] += d[i];
+  for (int i = 0; i < 4; ++i) acc[i] += (d[0][i] + d[1][i]) + (d[2][i] + d[3][i]);
 }
-__device__ __forceinline__ void few_chunk_f32(const char* stage, int kw, const char* x0,
-                                              const char* x1, int warp, int lane, float (&acc)[4]) {
-  const int g = lane >> 2;
-  const char* w0 = stage + g * kFewRowPitch;
+__device__ __forceinline__ void few_chunk_f32(uint32_t stage, int kw, uint32_t x0, uint32_t x1, int col,
+                                              int lane, float (&acc)[4]) {
+  const int r = few_row(lane >> 2);
   const float4 zero = make_float4(0, 0, 0, 0);
-  for (int kb = warp; kb < kw / 4; kb += kFewWarps) {
-    const float4 wa = *reinterpret_cast<const float4*>(w0 + kb * 16);
-    const float4 wb = *reinterpret_cast<const float4*>(w0 + 8 * kFewRowPitch + kb * 16);
-    const float4 xa = x0 ? *reinterpret_cast<const float4*>(x0 + kb * 16) : zero;
-    const float4 xb = x1 ? *reinterpret_cast<const float4*>(x1 + kb * 16) : zero;
+#pragma unroll 4
+  for (int kb = 0; kb < kw / 4; ++kb) {
+    const uint32_t w0 = stage + ((kb >> 3) * kFewRows + r) * 128 + (((kb & 7) ^ (r & 7)) << 4);
+    const float4 wa = lds128f(w0);
+    const float4 wb = lds128f(w0 + 8 * 128);
+    const float4 xa = x0 ? lds128f(x0 + (col + kb * 4) * 4) : zero;
+    const float4 xb = x1 ? lds128f(x1 + (col + kb * 4) * 4) : zero;
     acc[0] = fmaf(wa.x, xa.x, fmaf(wa.y, xa.y, fmaf(wa.z, xa.z, fmaf(wa.w, xa.w, acc[0]))));
     acc[1] = fmaf(wa.x, xb.x, fmaf(wa.y, xb.y, fmaf(wa.z, xb.z, fmaf(wa.w, xb.w, acc[1]))));
     acc[2] = fmaf(wb.x, xa.x, fmaf(wb.y, xa.y, fmaf(wb.z, xa.z, fmaf(wb.w, xa.w, acc[2]))));
@@ -380,11 +449,9 @@ __device__ __forceinline__ void few_topk(const FewParams& p, FewTables& tb, int 
       key[i] = ordered_key(kf);
     }
   }
-  float top_s[kMaxTopK];
-  float sum = 0.0f;
+  float mine = 0.0f, first = 0.0f;  // lane j: the j-th selected value
 #pragma unroll
   for (int j = 0; j < kMaxTopK; ++j) {
-    top_s[j] = 0.0f;
     if (j >= p.k) continue;
     uint32_t bk = 0u;
     int bi = 0x7fffffff;
@@ -395,51 +462,157 @@ __device__ __forceinline__ void few_topk(const FewParams& p, FewTables& tb, int 
     const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
     const uint32_t win =
         __reduce_min_sync(0xffffffffu, bk == m ? static_cast<uint32_t>(bi) : 0xffffffffu);
-    top_s[j] = __shfl_sync(0xffffffffu, bp, static_cast<int>(win & 31u));
-    // k <= n, and every candidate's key is above 0: some candidate is always left
-    if (lane == 0) tb.idx[t * p.k + j] = min(static_cast<int>(win), p.n - 1);
+    const float s = __shfl_sync(0xffffffffu, bp, static_cast<int>(win & 31u));
+    if (j == 0) first = s;
+    if (lane == j) {
+      mine = s;
+      // k <= n, and every candidate's key is above 0: some candidate is always left
+      tb.idx[t * p.k + j] = min(static_cast<int>(win), p.n - 1);
+    }
 #pragma unroll
     for (int i = 0; i < kMaxExperts / 32; ++i)
       if (static_cast<uint32_t>(lane + 32 * i) == win) key[i] = 0u;
   }
   bad = __any_sync(0xffffffffu, bad);
-  if (lane == 0) {
-    if (blockIdx.x == 0 && (bad || !(fabsf(top_s[0]) <= 3.0e38f))) latch_status(MOE_ERR_DEVICE_CHECK);
-    const bool sig = p.gate_mode == MOE_GATE_SIGMOID;
-    float ex[kMaxTopK];
+  if (lane == 0 && blockIdx.x == 0 && (bad || !(fabsf(first) <= 3.0e38f)))
+    latch_status(MOE_ERR_DEVICE_CHECK);
+  const bool sig = p.gate_mode == MOE_GATE_SIGMOID;
+  const float ex = lane < p.k ? (sig ? mine : expf(mine - first)) : 0.0f;
+  float sum = ex;
 #pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j) {
-      ex[j] = j < p.k ? (sig ? top_s[j] : expf(top_s[j] - top_s[0])) : 0.0f;
-      sum += ex[j];
-    }
-    const float denom = sig ? sum + 1e-15f : sum;
-#pragma unroll
-    for (int j = 0; j < kMaxTopK; ++j)
-      if (j < p.k) tb.w[t * p.k + j] = ex[j] / denom * p.routed_scale;
-  }
+  for (int o = kMaxTopK / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < p.k) tb.w[t * p.k + lane] = ex / (sig ? sum + 1e-15f : sum) * p.routed_scale;
 }
 
-// The layer.  Grid: one CTA per SM, cooperative (every CTA resident).
+// The routing tables of this CTA, by its multiplying warps, once every CTA's router tiles are done.
+__device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, volatile int* abort_,
+                                          uint64_t* routed, int warp, int lane) {
+  few_wait<FEW_MMA>(p.bar, 0, abort_);
+  if (warp < p.T) few_topk(p, tb, warp, lane);
+  few_bar<FEW_MMA>();
+  // distinct experts in ascending order, each with its slots in token order (thread = expert)
+  const int slots = p.T * p.k, tid = warp * 32 + lane;
+  unsigned long long hits = 0;  // slots routed to this thread's expert
+#pragma unroll 4
+  for (int s = 0; s < kFewSlots; s += 4) {
+    if (s >= slots) break;
+    const int4 v = *reinterpret_cast<const int4*>(&tb.idx[s]);  // entries past the last slot: masked
+    const unsigned f = (v.x == tid) | (v.y == tid) << 1 | (v.z == tid) << 2 | (v.w == tid) << 3;
+    hits |= static_cast<unsigned long long>(f) << s;
+  }
+  if (slots < 64) hits &= (1ull << slots) - 1ull;
+  const int cnt = min(__popcll(hits), kFewTokens);
+  const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
+  const unsigned most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(cnt));
+  if (lane == 0) {
+    tb.own[warp] = __popc(has);
+    tb.most[warp] = static_cast<int>(most);
+  }
+  few_bar<FEW_MMA>();
+  int at = __popc(has & ((1u << lane) - 1u)), total = 0, rows = 0;
+#pragma unroll
+  for (int w = 0; w < kFewMmaWarps; ++w) {
+    at += w < warp ? tb.own[w] : 0;
+    total += tb.own[w];
+    rows = max(rows, tb.most[w]);
+  }
+  if (cnt > 0) {
+    tb.expert[at] = tid;
+    tb.count[at] = cnt;
+    for (int q = 0; q < cnt; ++q) {
+      tb.slot[at][q] = static_cast<uint8_t>(__ffsll(hits) - 1);
+      hits &= hits - 1ull;
+    }
+  }
+  if (tid == 0) {
+    tb.dist = total;
+    tb.rows = p.resident ? p.T : rows;
+    if (p.L) {
+      const int pitch = max(few_row_pitch(false, p.E), few_row_pitch(false, p.H));
+      few_ring(p.pool_bytes - 2 * tb.rows * pitch, &tb.stages, &tb.turns);
+    } else {  // the first expert stage reads u where the router left it
+      tb.rows = p.T;
+      tb.stages = p.stages;
+      tb.turns = p.turns;
+    }
+  }
+  if (blockIdx.x == 0 && tid < slots) {
+    if (p.idx_out) p.idx_out[tid] = tb.idx[tid];
+    if (p.w_out) p.w_out[tid] = tb.w[tid];
+  }
+  few_bar<FEW_MMA>();
+  if (tid == 0) mbar_arrive(routed);
+}
+
+// A role's place in the ring: chunk c of the CTA's stream lies in stage (c - c0) % S, and warp
+// (c - c0) % W multiplies it.  The ring changes its depth between the dense and the expert stages (the
+// dense ones hold every token's row, the expert ones as many as one expert has); `bits` holds the
+// parity of the fills each stage had before.
+struct FewRing {
+  unsigned S, W, c0 = 0, bits = 0, c = 0;
+  __device__ FewRing(int s, int w) : S(s), W(w) {}
+  __device__ void at(unsigned chunk, unsigned& stage, unsigned& parity) const {
+    const unsigned q = (chunk - c0) / S;
+    stage = (chunk - c0) - q * S;
+    parity = (bits >> stage ^ q) & 1u;
+  }
+  __device__ void resize(int s, int w) {
+    const unsigned q = (c - c0) / S, r = (c - c0) - q * S;
+    if (q & 1u) bits ^= (1u << S) - 1u;
+    bits ^= (1u << r) - 1u;
+    c0 = c;
+    S = s;
+    W = w;
+  }
+};
+
+// Zeroes the grid-barrier and tile counters of one call.
+__global__ void few_init_kernel(unsigned* bar) {
+  pdl_wait();
+  pdl_launch_dependents();
+  for (int i = threadIdx.x; i < kFewBarriers * 16; i += blockDim.x) bar[i] = 0u;
+}
+
+// The layer.  Grid: one CTA per SM, cooperative (every CTA resident).  Warps 0-7 multiply: chunk c of
+// the CTA's stream (one ring stage) belongs to warp c % W (W <= 8), so W stages are in work at once and
+// a tile's chunks meet as up to W partial tiles in shared memory.  The ring holds a multiple
+// of W stages: then one warp alone waits on a stage's barrier, phase after phase (with another number
+// a warp could come to a stage whose previous fill has not landed, and take its parity for its own).  Warps 8-11 add the partial tiles
+// in chunk order and finish the tile (one barrier per tile among all warps had kept the stream at half
+// its rate).  Warp 12 is the producer.
 template <bool kF32>
-__global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewParams p) {
-  extern __shared__ __align__(128) uint8_t few_smem[];
-  char* act_mem = reinterpret_cast<char*>(few_smem);
-  char* ring = act_mem + p.act_bytes;
-  float* red = reinterpret_cast<float*>(ring + p.stages * kFewStageBytes);
-  float* s_v = red + 2 * kFewRedFloats;  // [T][rank] adapter inner products
+__global__ void __launch_bounds__(kFewThreads, 1)
+    few_layer_kernel(const FewParams p, const __grid_constant__ FewMaps maps) {
+  extern __shared__ uint8_t few_smem[];
+  char* ring = reinterpret_cast<char*>(few_smem) + ((0u - smem_u32(few_smem)) & 1023u);
+  char* act_mem = ring + p.stages * kFewStageBytes;  // dense stages; the expert stages' lies higher
+  float* red = reinterpret_cast<float*>(ring + p.pool_bytes);
+  float* s_v = red + kFewRedBufs * kFewRedFloats;  // [T][rank] adapter inner products
   __shared__ FewTables tb;
   __shared__ __align__(8) uint64_t full[kFewMaxStages], empty[kFewMaxStages], routed;
+  __shared__ __align__(8) uint64_t red_full[kFewRedBufs], red_empty[kFewRedBufs];
+  __shared__ __align__(8) uint64_t tq_full[kFewQueue], tq_empty[kFewQueue];
+  __shared__ int tq[kFewQueue];  // tiles taken from the shared counter; negative: no more
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int T = p.T, k = p.k;
   if (tid == 0) {
-    for (int s = 0; s < p.stages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], kFewWarps); }
+    for (int s = 0; s < kFewMaxStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < kFewRedBufs; ++b) {
+      mbar_init(&red_full[b], kFewMmaWarps);
+      mbar_init(&red_empty[b], kFewEpiWarps);
+    }
+    for (int q = 0; q < kFewQueue; ++q) {
+      mbar_init(&tq_full[q], 1);
+      mbar_init(&tq_empty[q], kFewMmaWarps + kFewEpiWarps);
+    }
     mbar_init(&routed, 1);
     fence_barrier_init();
     tb.abort_ = 0;
     tb.dist = 0;
     tb.ndist_ad = 0;
   }
+  pdl_wait();  // the counters are zeroed, and the inputs written, by kernels before this one
   if (tid < kFewTokens) {
     int a = p.nA && tid < T ? p.token_adapter[tid] : -1;
     if (a < -1 || a >= p.nA) {
@@ -460,92 +633,72 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewPara
     }
     __syncthreads();
   }
-  const FewTiles<kF32> tiles{p, tb};
+  const FewTiles<kF32> tiles{p, maps, tb};
   volatile int* abort_ = &tb.abort_;
+  constexpr int kPer = kFewBlocks * 128 / (kF32 ? 4 : 2);  // values of a row per chunk
 
-  if (warp == kFewWarps) {
+  if (warp == kFewMmaWarps + kFewEpiWarps) {
     // -------------------------------------------------------------- producer
-    constexpr int kEs = kF32 ? 4 : 2;
-    uint32_t stage = 0, phase_bit = 0, issued = 0, parities = 0;
+    if (lane != 0) return;
+    constexpr int kCols = 128 / (kF32 ? 4 : 2);
+    // every weight is read once: its lines go first when L2 needs room, and the stages' small
+    // intermediates stay (one token of the Muse layer: 181 us with it, 192 without)
+    const uint64_t policy = l2_policy_evict_first();
+    FewRing rg(p.stages, p.turns);
+    unsigned issued = 0, parities = 0, qn = 0;
     bool ok = true;
+    auto issue = [&](const FewTile& t) {
+      for (int kb = 0; kb < t.K / kCols && ok; kb += kFewBlocks) {
+        unsigned stage, parity;
+        rg.at(rg.c++, stage, parity);
+        if (!mbar_wait(&empty[stage], parity ^ 1u)) { ok = false; break; }
+        mbar_arrive_expect_tx(&full[stage], kFewStageBytes);
+        tma_load_4d(t.map, &full[stage], ring + stage * kFewStageBytes, 0, t.row, t.half, kb, policy);
+        issued |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | (parity << stage);
+      }
+    };
     for (int ph = FEW_IN; ph <= FEW_OUT && ok; ++ph) {
-      if (ph == FEW_UP1) ok = mbar_wait(&routed, 0);
+      if (ph == FEW_UP1) {
+        // the routing is known, and no warp reads the dense stages' activations any more
+        ok = mbar_wait(&routed, 0);
+        rg.resize(tb.stages, tb.turns);
+      } else if (ph == FEW_OUT) {
+        rg.resize(p.stages, p.turns);
+      }
       if (!ok) break;
+      const int N = tiles.total(ph), fixed = tiles.fixed(ph);
       int i, end, step;
       tiles.range(ph, i, end, step);
-      for (; i < end && ok; i += step) {
-        const FewTile t = tiles.get(ph, i);
-        const int row = min(lane, t.valid - 1);
-        const char* src = row < t.split ? t.base + row * t.ld_bytes
-                                        : t.base2 + (row - t.split) * t.ld_bytes;
-        for (int seg = 0; seg < t.segs && ok; ++seg) {
-          const int seg_bytes = t.seg_len * kEs;
-          for (int o = 0; o < seg_bytes; o += kFewRowBytes) {
-            const int bytes = min(kFewRowBytes, seg_bytes - o);
-            if (!mbar_wait(&empty[stage], phase_bit ^ 1)) { ok = false; break; }
-            if (lane == 0) mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(bytes) * kFewRows);
-            __syncwarp();
-            if (lane < kFewRows)
-              bulk_load(ring + stage * kFewStageBytes + lane * kFewRowPitch,
-                        src + static_cast<long>(seg) * seg_bytes + o, static_cast<uint32_t>(bytes),
-                        &full[stage]);
-            issued |= 1u << stage;
-            parities = (parities & ~(1u << stage)) | (phase_bit << stage);
-            if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase_bit ^= 1; }
-          }
-        }
+      unsigned* counter = p.bar + (ph == FEW_UP1 ? 7 : 8) * 16;
+      // a counter's answer takes about a tile's time to come: it is asked for one tile ahead
+      int next = fixed < N ? static_cast<int>(atomicAdd(counter, 1u)) : N;
+      for (; i < end && ok; i += step) issue(tiles.get(ph, i));
+      while (fixed < N && ok) {
+        const int j = fixed + next < N ? fixed + next : -1;
+        if (j >= 0) next = static_cast<int>(atomicAdd(counter, 1u));
+        const unsigned q = qn % kFewQueue;
+        if (!mbar_wait(&tq_empty[q], (qn / kFewQueue & 1u) ^ 1u)) { ok = false; break; }
+        tq[q] = j;
+        mbar_arrive(&tq_full[q]);
+        ++qn;
+        if (j < 0) break;
+        issue(tiles.get(ph, j));
       }
     }
     if (!ok) *abort_ = 1;
     // No copy may still be landing in shared memory when the CTA exits.
-    for (int s = 0; s < p.stages; ++s)
+    for (int s = 0; s < kFewMaxStages; ++s)
       if (issued >> s & 1) mbar_wait(&full[s], parities >> s & 1);
     return;
   }
 
-  // ---------------------------------------------------------------- consumers
-  uint32_t stage = 0, phase_bit = 0;
-  int red_buf = 0;
-  // Runs one tile through the ring; on return the 16 x 8 tile's partial sums of every warp lie in
-  // the returned buffer.  arow of column c is rows[c]'s activation row, or none.
-  auto run_tile = [&](const FewTile& t, const FewAct& act, int my_row, int row0, int row1) -> const float* {
-    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    constexpr int kPer = kFewRowBytes / (kF32 ? 4 : 2);
-    for (int seg = 0; seg < t.segs; ++seg) {
-      for (int k0 = 0; k0 < t.seg_len; k0 += kPer) {
-        if (!*abort_ && !mbar_wait(&full[stage], phase_bit)) *abort_ = 1;
-        const char* st = ring + stage * kFewStageBytes;
-        const int kw = min(kPer, t.seg_len - k0);
-        if constexpr (kF32) {
-          const char* x0 = row0 >= 0 ? act.base + row0 * act.pitch + k0 * 4 : nullptr;
-          const char* x1 = row1 >= 0 ? act.base + row1 * act.pitch + k0 * 4 : nullptr;
-          few_chunk_f32(st, kw, x0, x1, warp, lane, acc);
-        } else {
-          const char* ar = my_row >= 0 ? act.base + my_row * act.pitch + k0 * 2 : nullptr;
-          few_chunk_bf16(st, kw, ar, act.plane, warp, lane, acc);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[stage]);
-        if (++stage == static_cast<uint32_t>(p.stages)) { stage = 0; phase_bit ^= 1; }
-      }
-    }
-    float* rb = red + red_buf * kFewRedFloats;
-    red_buf ^= 1;
-    float* mine = rb + warp * kFewRows * kFewRedPitch;
-    const int g = lane >> 2, c = (lane & 3) * 2;
-    *reinterpret_cast<float2*>(mine + g * kFewRedPitch + c) = make_float2(acc[0], acc[1]);
-    *reinterpret_cast<float2*>(mine + (g + 8) * kFewRedPitch + c) = make_float2(acc[2], acc[3]);
-    few_bar();
-    return rb;
-  };
-  auto tile_sum = [&](const float* rb, int row, int col) {
-    float v = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kFewWarps; ++w) v += rb[(w * kFewRows + row) * kFewRedPitch + col];
-    return v;
-  };
-  const int er = tid & 15, ec = tid >> 4;  // epilogue: tile row and column (threads 0 .. 127)
-  const int g8 = lane >> 2, t2 = (lane & 3) * 2;
+  const bool mma = warp < kFewMmaWarps;
+  const int et = tid - kFewMma;            // thread of the finishing group
+  const int er = et & 15, ec = et >> 4;    // its tile row and column
+  FewRing rg(p.stages, p.turns);
+  unsigned tile_no = 0, qn = 0;
+  FewAct act;
 
   // Residual gate and store of one output value.
   auto resid_out = [&](int t, int f, float b) {
@@ -565,34 +718,6 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewPara
       static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.d + f] = f32_to_bf16(x);
     }
   };
-
-  // u (or C_in(r)) to shared memory
-  FewAct act = few_act<kF32>(act_mem, T, p.d, false);
-  {
-    const void* src = p.input_norm ? p.r : p.u;
-    const int vec = p.d * (kF32 ? 4 : 2) / 16;
-    for (int t = 0; t < T; ++t) {
-      const uint4* row = static_cast<const uint4*>(src) + static_cast<size_t>(t) * vec;
-      char* dst = act.base + t * act.pitch;
-      for (int i = tid; i < vec; i += 32 * kFewWarps) *reinterpret_cast<uint4*>(dst + i * 16) = row[i];
-    }
-    few_bar();
-    if constexpr (!kF32) {
-      if (p.input_norm && warp < T) {  // one warp per token
-        uint16_t* row = reinterpret_cast<uint16_t*>(act.base + warp * act.pitch);
-        float ss = 0.0f;
-        for (int i = lane; i < p.d; i += 32) { const float x = bf16_to_f32(row[i]); ss = fmaf(x, x, ss); }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        const float inv = 1.0f / sqrtf(ss / p.d + p.eps_block);
-        for (int i = lane; i < p.d; i += 32)
-          row[i] = f32_to_bf16((1.0f + p.gamma_in[i]) * (bf16_to_f32(row[i]) * inv));
-      }
-      few_bar();
-    }
-  }
-  const int tok_row = g8 < T ? g8 : -1, tok_row0 = t2 < T ? t2 : -1, tok_row1 = t2 + 1 < T ? t2 + 1 : -1;
-
   // The adapter term of row f for token t (0 without an adapter): sum over the rank in fp32.
   auto adapter_term = [&](const uint16_t* bmat, int rows, int f, int t) {
     const int a = tb.tok_ad[t];
@@ -608,294 +733,332 @@ __global__ void __launch_bounds__(kFewThreads, 1) few_layer_kernel(const FewPara
     }
     return v;
   };
-  auto load_v = [&](const float* v) {
-    for (int i = tid; i < T * p.rank; i += 32 * kFewWarps) s_v[i] = __ldcg(&v[i]);
-    few_bar();
+  // Sum over the 16 rows of this thread's tile column.
+  auto column_sum = [](float q) {
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+    return q;
   };
-  // Inner products of an adapter tile: scale * (A x), for the tokens that use this adapter.
-  auto put_v = [&](const FewTile& t, const float* rb, float* v) {
-    if (tid < 128 && ec < T && er < t.valid && tb.tok_ad[ec] == tb.ad[t.e])
-      v[ec * p.rank + t.r0 + er] = p.scale[tb.ad[t.e]] * tile_sum(rb, er, ec);
+  // Rows of fp32 values from global memory into the activation region, by the multiplying warps.
+  auto load_rows = [&](int rows, int K, const float* src, auto row_of, const float* gain) {
+    const int vec = K / 4;
+    for (int i = tid; i < rows * vec; i += kFewMma) {
+      const int row = i / vec, c = (i - row * vec) * 4;
+      float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(row_of(row)) * K + c));
+      if (gain) {
+        const float4 g = *reinterpret_cast<const float4*>(gain + c);
+        v.x *= 1.0f + g.x; v.y *= 1.0f + g.y; v.z *= 1.0f + g.z; v.w *= 1.0f + g.w;
+      }
+      few_act_put4<kF32>(act, row, c, v);
+    }
+    few_bar<FEW_MMA>();
   };
 
-  // -------------------------------------------------------------- router, adapters' A, latent down
-  {
-    int i, end, step;
-    tiles.range(FEW_IN, i, end, step);
-    const int lead = tiles.lead_tiles(FEW_IN);
-    for (; i < lead; i += step) {
-      const FewTile t = tiles.get(FEW_IN, i);
-      const float* rb = run_tile(t, act, tok_row, tok_row0, tok_row1);
-      if (t.kind == FEW_ROUTER) {
-        const int e = t.r0 + er;
-        if (tid < 128 && ec < T && e < p.n) {
-          float l = tile_sum(rb, er, ec);
-          if (p.gate_mode == MOE_GATE_SIGMOID) l *= p.logit_mult;
-          p.logits[static_cast<size_t>(ec) * p.n + e] = l + (p.logit_bias ? p.logit_bias[e] : 0.0f);
-        }
-      } else {
-        put_v(t, rb, p.v_down);
+  for (int ph = FEW_IN; ph <= FEW_OUT; ++ph) {
+    // ------------------------------------------------------------ what the stage multiplies
+    if (ph == FEW_IN) {  // u, or C_in(r)
+      act = few_act<kF32>(act_mem, T, p.d, false);
+      const void* src = p.input_norm ? p.r : p.u;
+      const int vec = p.d * (kF32 ? 4 : 2) / 16;
+      for (int t = 0; t < T; ++t) {
+        const uint4* row = static_cast<const uint4*>(src) + static_cast<size_t>(t) * vec;
+        char* dst = act.base + t * act.pitch;
+        for (int i = tid; i < vec; i += kFewWork) *reinterpret_cast<uint4*>(dst + i * 16) = row[i];
       }
-    }
-    few_arrive(p.bar, 0);
-    bool have_v = tb.ndist_ad == 0;
-    for (; i < end; i += step) {
-      const FewTile t = tiles.get(FEW_IN, i);
-      const float* rb = run_tile(t, act, tok_row, tok_row0, tok_row1);
-      if (!have_v) {
-        few_wait(p.bar, 0, abort_);
-        load_v(p.v_down);
-        have_v = true;
-      }
-      if (tid < 128 && ec < T) {
-        float v = tile_sum(rb, er, ec);
-        if (tb.ndist_ad) v += adapter_term(p.down_b, p.L, t.r0 + er, ec);
-        p.z[static_cast<size_t>(ec) * p.L + t.r0 + er] = v;
-      }
-    }
-    few_arrive(p.bar, 1);
-  }
-
-  // -------------------------------------------------------------- routing tables
-  few_wait(p.bar, 0, abort_);
-  if (warp < T) few_topk(p, tb, warp, lane);
-  few_bar();
-  {
-    // distinct experts in ascending order, each with its slots in token order (thread = expert)
-    const int slots = T * k;
-    int cnt = 0;
-    uint8_t mine[kFewTokens];
-    for (int s = 0; s < slots; ++s)
-      if (tb.idx[s] == tid && cnt < kFewTokens) mine[cnt++] = static_cast<uint8_t>(s);
-    tb.own[tid] = cnt;
-    few_bar();
-    if (cnt > 0) {
-      int at = 0;
-      for (int e = 0; e < tid; ++e) at += tb.own[e] > 0;
-      tb.expert[at] = tid;
-      tb.count[at] = cnt;
-      for (int q = 0; q < cnt; ++q) tb.slot[at][q] = mine[q];
-    }
-    if (tid == 255) {
-      int at = 0;
-      for (int e = 0; e < 256; ++e) at += tb.own[e] > 0;
-      tb.dist = at;
-    }
-    if (blockIdx.x == 0 && tid < slots) {
-      if (p.idx_out) p.idx_out[tid] = tb.idx[tid];
-      if (p.w_out) p.w_out[tid] = tb.w[tid];
-    }
-    few_bar();
-    if (tid == 0) mbar_arrive(&routed);
-  }
-
-  // -------------------------------------------------------------- z (C_pre) to shared memory
-  if (p.L) {
-    few_wait(p.bar, 1, abort_);
-    act = few_act<kF32>(act_mem, T, p.E, true);
-    if (p.pre_norm) {
-      float ss[kFewTokens];
+      few_bar<FEW_WORK>();
+      if constexpr (!kF32) {
+        if (p.input_norm) {
+          if (warp < T) {  // one warp per token
+            uint16_t* row = reinterpret_cast<uint16_t*>(act.base + warp * act.pitch);
+            float ss = 0.0f;
+            for (int i = lane; i < p.d; i += 32) { const float x = bf16_to_f32(row[i]); ss = fmaf(x, x, ss); }
 #pragma unroll
-      for (int t = 0; t < kFewTokens; ++t) {
-        ss[t] = 0.0f;
-        if (t < T)
-          for (int c = tid * 4; c < p.E; c += 128 * kFewWarps) {
-            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.z + static_cast<size_t>(t) * p.E + c));
-            ss[t] += v.x * v.x + v.y * v.y + v.z * v.z + v.w * v.w;
+            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float inv = 1.0f / sqrtf(ss / p.d + p.eps_block);
+            for (int i = lane; i < p.d; i += 32)
+              row[i] = f32_to_bf16((1.0f + p.gamma_in[i]) * (bf16_to_f32(row[i]) * inv));
           }
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) ss[t] += __shfl_xor_sync(0xffffffffu, ss[t], o);
-        if (lane == 0) tb.red[warp][t] = ss[t];
-      }
-      few_bar();
-      if (tid < T) {
-        float v = 0.0f;
-        for (int w = 0; w < kFewWarps; ++w) v += tb.red[w][tid];
-        tb.norm[tid] = 1.0f / sqrtf(v / p.E + p.eps);
-      }
-      few_bar();
-    }
-    for (int t = 0; t < T; ++t) {
-      const float inv = p.pre_norm ? tb.norm[t] : 1.0f;
-      for (int c = tid * 4; c < p.E; c += 128 * kFewWarps) {
-        float4 v = __ldcg(reinterpret_cast<const float4*>(p.z + static_cast<size_t>(t) * p.E + c));
-        if (p.pre_norm) {
-          const float4 g = *reinterpret_cast<const float4*>(p.gamma_pre + c);
-          v.x *= inv * (1.0f + g.x); v.y *= inv * (1.0f + g.y);
-          v.z *= inv * (1.0f + g.z); v.w *= inv * (1.0f + g.w);
-        }
-        few_act_put4<kF32>(act, t, c, v);
-      }
-    }
-    few_bar();
-  }
-
-  // -------------------------------------------------------------- experts, first product
-  {
-    int i, end, step;
-    tiles.range(FEW_UP1, i, end, step);
-    for (; i < end; i += step) {
-      const FewTile t = tiles.get(FEW_UP1, i);
-      const int m = tb.count[t.e];
-      auto tok = [&](int c) { return c < m ? tb.slot[t.e][c] / k : -1; };
-      const float* rb = run_tile(t, act, tok(g8), tok(t2), tok(t2 + 1));
-      if (p.swiglu) {
-        if (tid < 64) {
-          const int row = tid & 7, col = tid >> 3;
-          if (col < m) {
-            const float g = tile_sum(rb, row, col), up = tile_sum(rb, row + 8, col);
-            p.a[static_cast<size_t>(tb.slot[t.e][col]) * p.H + t.r0 + row] = g / (1.0f + expf(-g)) * up;
-          }
-        }
-      } else if (tid < 128 && ec < m) {
-        const float v = tile_sum(rb, er, ec);
-        // NaN stays NaN (fmaxf would drop it)
-        p.a[static_cast<size_t>(tb.slot[t.e][ec]) * p.H + t.r0 + er] = v < 0.0f ? 0.0f : v;
-      }
-    }
-    few_arrive(p.bar, 2);
-  }
-
-  // -------------------------------------------------------------- experts, second product
-  few_wait(p.bar, 2, abort_);
-  {
-    int i, end, step, loaded = -1;
-    tiles.range(FEW_DOWN2, i, end, step);
-    act = few_act<kF32>(act_mem, T, p.H, true);
-    for (; i < end; i += step) {
-      const FewTile t = tiles.get(FEW_DOWN2, i);
-      const int m = tb.count[t.e];
-      if (t.e != loaded) {  // this expert's rows (every warp is past the previous tile's products)
-        for (int c = 0; c < m; ++c) {
-          const float* row = p.a + static_cast<size_t>(tb.slot[t.e][c]) * p.H;
-          for (int j = tid * 4; j < p.H; j += 128 * kFewWarps)
-            few_act_put4<kF32>(act, c, j, __ldcg(reinterpret_cast<const float4*>(row + j)));
-        }
-        few_bar();
-        loaded = t.e;
-      }
-      const float* rb = run_tile(t, act, g8 < m ? g8 : -1, t2 < m ? t2 : -1, t2 + 1 < m ? t2 + 1 : -1);
-      if (tid < 128) {
-        const int f = t.r0 + er;
-        float v = 0.0f;
-        if (ec < m) {
-          v = tile_sum(rb, er, ec);
-          if (p.expert_norm) v *= 1.0f + p.gamma_expert[f];
-          p.s[static_cast<size_t>(tb.slot[t.e][ec]) * p.E + f] = v;
-        }
-        if (p.expert_norm) {
-          float q = v * v;
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-          if (er == 0 && ec < m)
-            p.ss[static_cast<size_t>(tb.slot[t.e][ec]) * (p.E / 16) + t.r0 / 16] = q;
+          few_bar<FEW_WORK>();
         }
       }
-    }
-    few_arrive(p.bar, 3);
-  }
-
-  // -------------------------------------------------------------- I_gamma and the weighted sum
-  few_wait(p.bar, 3, abort_);
-  {
-    const int cols = 32 * kFewWarps, blocks = (p.E + cols - 1) / cols;
-    for (int unit = blockIdx.x; unit < T * blocks; unit += gridDim.x) {
-      const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
-      if (warp < k) {
-        float inv = 1.0f;
-        if (p.expert_norm) {
-          const float* part = p.ss + static_cast<size_t>(t * k + warp) * (p.E / 16);
+    } else if (ph == FEW_UP1) {
+      // The routing tables, by the multiplying warps; then (1 + gamma_pre) z.  C_pre's 1/rms is one
+      // factor per token, applied when a tile is finished.  Without latent projections the products
+      // take u, which is there already.
+      if (mma) few_route(p, tb, abort_, &routed, warp, lane);
+      few_wait<FEW_WORK>(p.bar, 1, abort_);
+      rg.resize(tb.stages, tb.turns);
+      act_mem = ring + tb.stages * kFewStageBytes;
+      if (p.L) act = few_act<kF32>(act_mem, tb.rows, p.E, true);
+      if (mma) {
+        if (p.L && p.resident)
+          load_rows(T, p.E, p.z, [](int c) { return c; }, p.pre_norm ? p.gamma_pre : nullptr);
+      } else if (p.pre_norm) {
+        for (int t = warp - kFewMmaWarps; t < T; t += kFewEpiWarps) {
           float q = 0.0f;
-          for (int j = lane; j < p.E / 16; j += 32) q += __ldcg(&part[j]);
+          for (int j = lane; j < p.L / 16; j += 32) q += __ldcg(&p.zss[static_cast<size_t>(t) * (p.L / 16) + j]);
 #pragma unroll
           for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-          inv = 1.0f / sqrtf(q / p.E + p.eps);
+          if (lane == 0) tb.norm[t] = 1.0f / sqrtf(q / p.L + p.eps);
         }
-        if (lane == 0) tb.inv[warp] = inv;
+        few_bar<FEW_EPI>();
       }
-      few_bar();
-      if (c < p.E) {
-        float y = 0.0f;
-        for (int j = 0; j < k; ++j)
-          y = fmaf(tb.w[t * k + j],
-                   __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) * tb.inv[j], y);
-        if (p.L) p.y[static_cast<size_t>(t) * p.E + c] = y;
-        else if (kF32) static_cast<float*>(p.out)[static_cast<size_t>(t) * p.E + c] = y;
-        else static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.E + c] = f32_to_bf16(y);
+    } else if (ph == FEW_DOWN2) {
+      act = few_act<kF32>(act_mem, tb.rows, p.H, true);
+      if (mma) few_wait<FEW_MMA>(p.bar, 2, abort_);
+    } else {
+      // I_gamma and the weighted sum: y, or without latent projections the layer's output
+      few_wait<FEW_WORK>(p.bar, 3, abort_);
+      const int cols = kFewMma, blocks = (p.E + cols - 1) / cols;
+      for (int unit = blockIdx.x; unit < T * blocks; unit += gridDim.x) {
+        const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
+        if (warp < k) {
+          float inv = 1.0f;
+          if (p.expert_norm) {
+            const float* part = p.ss + static_cast<size_t>(t * k + warp) * (p.E / 16);
+            float q = 0.0f;
+            for (int j = lane; j < p.E / 16; j += 32) q += __ldcg(&part[j]);
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+            inv = 1.0f / sqrtf(q / p.E + p.eps);
+          }
+          if (lane == 0) tb.inv[warp] = inv;
+        }
+        few_bar<FEW_WORK>();
+        if (mma && c < p.E) {
+          float y = 0.0f;
+          for (int j = 0; j < k; ++j)
+            y = fmaf(tb.w[t * k + j],
+                     __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) * tb.inv[j], y);
+          if (p.L) p.y[static_cast<size_t>(t) * p.E + c] = y;
+          else if (kF32) static_cast<float*>(p.out)[static_cast<size_t>(t) * p.E + c] = y;
+          else static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.E + c] = f32_to_bf16(y);
+        }
+        few_bar<FEW_WORK>();
       }
-      few_bar();
+      if (!p.L) return;
+      few_arrive<FEW_WORK>(p.bar, 4);
+      few_wait<FEW_WORK>(p.bar, 4, abort_);
+      rg.resize(p.stages, p.turns);
+      act_mem = ring + p.stages * kFewStageBytes;
+      act = few_act<kF32>(act_mem, T, p.L, true);
+      for (int t = 0; t < T; ++t)
+        for (int c = tid * 4; c < p.L; c += 4 * kFewWork)
+          few_act_put4<kF32>(act, t, c, __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(t) * p.L + c)));
+      few_bar<FEW_WORK>();
     }
-  }
-  if (!p.L) return;
-  few_arrive(p.bar, 4);
-  few_wait(p.bar, 4, abort_);
 
-  // -------------------------------------------------------------- adapters' A', latent up, residual
-  act = few_act<kF32>(act_mem, T, p.L, true);
-  for (int t = 0; t < T; ++t)
-    for (int c = tid * 4; c < p.L; c += 128 * kFewWarps)
-      few_act_put4<kF32>(act, t, c, __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(t) * p.L + c)));
-  few_bar();
-  {
+    // ------------------------------------------------------------ the stage's tiles
+    const bool expert = ph == FEW_UP1 || ph == FEW_DOWN2;
+    const bool shared_counter = tiles.fixed(ph) != tiles.total(ph);
+    const int lead = expert ? 0 : tiles.lead_tiles(ph), lead_bar = ph == FEW_IN ? 0 : 5;
+    bool lead_done = expert || (ph == FEW_OUT && tb.ndist_ad == 0), have_v = tb.ndist_ad == 0;
+    int loaded = -1;
     int i, end, step;
-    tiles.range(FEW_OUT, i, end, step);
-    const int lead = tiles.lead_tiles(FEW_OUT);
-    for (; i < lead; i += step) {
-      const FewTile t = tiles.get(FEW_OUT, i);
-      put_v(t, run_tile(t, act, tok_row, tok_row0, tok_row1), p.v_up);
-    }
-    bool have_v = tb.ndist_ad == 0;
-    if (!have_v) few_arrive(p.bar, 5);
-    for (; i < end; i += step) {
-      const FewTile t = tiles.get(FEW_OUT, i);
-      const float* rb = run_tile(t, act, tok_row, tok_row0, tok_row1);
-      if (!have_v) {
-        few_wait(p.bar, 5, abort_);
-        load_v(p.v_up);
-        have_v = true;
+    tiles.range(ph, i, end, step);
+    for (;; i += step) {
+      int j = i;
+      if (i >= end) {  // the tiles the producer takes from the shared counter
+        if (!shared_counter) break;
+        const unsigned q = qn % kFewQueue;
+        if (!*abort_ && !mbar_wait(&tq_full[q], qn / kFewQueue & 1u)) *abort_ = 1;
+        j = *abort_ ? -1 : *static_cast<volatile int*>(&tq[q]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tq_empty[q]);
+        ++qn;
+        if (j < 0) break;
       }
-      if (tid < 128) {
-        const int f = t.r0 + er;
-        float v = 0.0f;
-        if (ec < T) {
-          v = tile_sum(rb, er, ec);
-          if (tb.ndist_ad) v += adapter_term(p.up_b, p.d, f, ec);
-          if (p.post_norm) {
-            v *= 1.0f + p.gamma_post[f];
-            p.b[static_cast<size_t>(ec) * p.d + f] = v;
+      const FewTile t = tiles.get(ph, j);
+      const int m = expert ? tb.count[t.e] : T;  // activation rows of this tile
+      const unsigned rb = tile_no % kFewRedBufs, rturn = tile_no / kFewRedBufs & 1u;
+      ++tile_no;
+      const int nch = (t.K + kPer - 1) / kPer;
+      // With a lo plane and at most four rows, MMA columns 4 .. 7 take the rows' lo planes and the
+      // finishing group adds columns c and c + 4: half the products of a second pass over the weights.
+      const bool pair = act.plane && m <= 4;
+
+      if (mma) {
+        const bool per_expert = ph == FEW_DOWN2 || (ph == FEW_UP1 && p.L && !p.resident);
+        if (per_expert && t.e != loaded) {  // its rows, once every warp is past the previous ones
+          few_bar<FEW_MMA>();
+          if (ph == FEW_UP1)
+            load_rows(m, p.E, p.z, [&](int c) { return tb.slot[t.e][c] / k; }, p.pre_norm ? p.gamma_pre : nullptr);
+          else
+            load_rows(m, p.H, p.a, [&](int c) { return static_cast<int>(tb.slot[t.e][c]); }, nullptr);
+          loaded = t.e;
+        }
+        const int W = static_cast<int>(rg.W), turn0 = static_cast<int>((rg.c - rg.c0) % rg.W);
+        const int first = warp - turn0 + (warp < turn0 ? W : 0);
+        const bool part = warp < W && first < nch;
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (part) {
+          const uint32_t abase = smem_u32(act.base);
+          auto row_at = [&](int c) {  // activation row of column c
+            const int row = ph == FEW_UP1 && !per_expert ? tb.slot[t.e][c] / k : c;
+            return abase + static_cast<uint32_t>(row * act.pitch);
+          };
+          uint32_t xa = 0, xb = 0;
+          if constexpr (kF32) {
+            const int c = (lane & 3) * 2;
+            if (c < m) xa = row_at(c);
+            if (c + 1 < m) xb = row_at(c + 1);
           } else {
-            resid_out(ec, f, v);
+            const int g = lane >> 2;
+            if (pair) {
+              if ((g & 3) < m) xa = row_at(g & 3) + (g >> 2) * act.plane;
+            } else if (g < m) {
+              xa = row_at(g);
+              xb = xa + act.plane;
+            }
+          }
+          for (int ci = first; ci < nch; ci += W) {
+            unsigned stage, parity;
+            rg.at(rg.c + ci, stage, parity);
+            if (!*abort_ && !mbar_wait(&full[stage], parity)) *abort_ = 1;
+            const uint32_t st = smem_u32(ring) + stage * kFewStageBytes;
+            const int k0 = ci * kPer, kw = min(kPer, t.K - k0);
+            if constexpr (kF32) {
+              few_chunk_f32(st, kw, xa, xb, k0, lane, acc);
+            } else {
+              const int col = t.wrap == t.K ? k0 : k0 % t.wrap;
+              if (act.plane && !pair) few_chunk_bf16<true>(st, kw, xa, xb, col, t.wrap, lane, acc);
+              else few_chunk_bf16<false>(st, kw, xa, 0, col, t.wrap, lane, acc);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&empty[stage]);
           }
         }
-        if (p.post_norm) {
-          float q = v * v;
-#pragma unroll
-          for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-          if (er == 0 && ec < T) p.bss[static_cast<size_t>(ec) * (p.d / 16) + t.r0 / 16] = q;
+        if (!*abort_ && !mbar_wait(&red_empty[rb], rturn ^ 1u)) *abort_ = 1;
+        if (part) {
+          float* mine = red + rb * kFewRedFloats + first * kFewRows * kFewRedPitch;
+          const int g = few_row(lane >> 2), c = (lane & 3) * 2;
+          *reinterpret_cast<float2*>(mine + g * kFewRedPitch + c) = make_float2(acc[0], acc[1]);
+          *reinterpret_cast<float2*>(mine + (g + 8) * kFewRedPitch + c) = make_float2(acc[2], acc[3]);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&red_full[rb]);
+        rg.c += nch;
+        continue;
+      }
+
+      // ---- finishing group
+      if (!lead_done && j >= lead) {
+        few_arrive<FEW_EPI>(p.bar, lead_bar);
+        lead_done = true;
+      }
+      if (!have_v && j >= lead && !expert) {  // the adapters' inner products
+        few_wait<FEW_EPI>(p.bar, lead_bar, abort_);
+        const float* v = ph == FEW_IN ? p.v_down : p.v_up;
+        for (int x = et; x < T * p.rank; x += kFewEpi) s_v[x] = __ldcg(&v[x]);
+        few_bar<FEW_EPI>();
+        have_v = true;
+      }
+      const bool dual = t.kind == FEW_GATEUP && p.swiglu;
+      // SwiGLU tiles: 16 columns of 8 features, of which the upper columns are empty
+      const int row = dual ? et & 7 : er, col = dual ? et >> 3 : ec;
+      const int f = t.r0 + row;
+      const float gain = t.kind == FEW_EXPERT_OUT && p.expert_norm ? 1.0f + p.gamma_expert[f] : 1.0f;
+      // the tile's value at (row, col), and at (row + 8, col)
+      if (!*abort_ && !mbar_wait(&red_full[rb], rturn)) *abort_ = 1;
+      float v = 0.0f, up = 0.0f;
+      {
+        const float* at = red + rb * kFewRedFloats + row * kFewRedPitch + min(col, kFewTokens - 1);
+        const int parts = min(nch, static_cast<int>(rg.W));
+        for (int q = 0; q < parts; ++q, at += kFewRows * kFewRedPitch) {
+          v += at[0];
+          if (dual) up += at[8 * kFewRedPitch];
+          if (pair && col < 4) {
+            v += at[4];
+            if (dual) up += at[8 * kFewRedPitch + 4];
+          }
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&red_empty[rb]);
+      const bool mine = col < m;
+      switch (t.kind) {
+        case FEW_ROUTER:
+          if (mine && f < p.n) {
+            if (p.gate_mode == MOE_GATE_SIGMOID) v *= p.logit_mult;
+            p.logits[static_cast<size_t>(col) * p.n + f] = v + (p.logit_bias ? p.logit_bias[f] : 0.0f);
+          }
+          break;
+        case FEW_AD_DOWN:
+        case FEW_AD_UP:  // inner products scale * (A x), for the tokens that use this adapter
+          if (mine && row < t.valid && tb.tok_ad[col] == tb.ad[t.e])
+            (ph == FEW_IN ? p.v_down : p.v_up)[col * p.rank + f] = p.scale[tb.ad[t.e]] * v;
+          break;
+        case FEW_LATENT:
+          if (mine) {
+            if (tb.ndist_ad) v += adapter_term(p.down_b, p.L, f, col);
+            p.z[static_cast<size_t>(col) * p.L + f] = v;
+          }
+          if (p.pre_norm) {
+            const float q = column_sum(v * v);
+            if (row == 0 && mine) p.zss[static_cast<size_t>(col) * (p.L / 16) + t.r0 / 16] = q;
+          }
+          break;
+        case FEW_GATEUP:
+          if (mine) {
+            const int slot = tb.slot[t.e][col];
+            const float inv = p.pre_norm ? tb.norm[slot / k] : 1.0f;
+            v *= inv;
+            if (dual) v = v / (1.0f + expf(-v)) * (up * inv);
+            else v = v < 0.0f ? 0.0f : v;  // NaN stays NaN (fmaxf would drop it)
+            p.a[static_cast<size_t>(slot) * p.H + f] = v;
+          }
+          break;
+        case FEW_EXPERT_OUT: {
+          v *= gain;
+          const int slot = mine ? tb.slot[t.e][col] : 0;
+          if (mine) p.s[static_cast<size_t>(slot) * p.E + f] = v;
+          if (p.expert_norm) {
+            const float q = column_sum(v * v);
+            if (row == 0 && mine) p.ss[static_cast<size_t>(slot) * (p.E / 16) + t.r0 / 16] = q;
+          }
+          break;
+        }
+        default:  // FEW_LAYER_OUT
+          if (mine) {
+            if (tb.ndist_ad) v += adapter_term(p.up_b, p.d, f, col);
+            if (p.post_norm) {
+              v *= 1.0f + p.gamma_post[f];
+              p.b[static_cast<size_t>(col) * p.d + f] = v;
+            } else {
+              resid_out(col, f, v);
+            }
+          }
+          if (p.post_norm) {
+            const float q = column_sum(v * v);
+            if (row == 0 && mine) p.bss[static_cast<size_t>(col) * (p.d / 16) + t.r0 / 16] = q;
+          }
+      }
+    }
+    if (!mma) {
+      if (!lead_done) few_arrive<FEW_EPI>(p.bar, lead_bar);
+      if (ph != FEW_OUT) few_arrive<FEW_EPI>(p.bar, ph == FEW_IN ? 1 : ph == FEW_UP1 ? 2 : 3);
     }
   }
   if (!p.post_norm) return;
 
   // -------------------------------------------------------------- output norm, residual
-  few_arrive(p.bar, 6);
-  few_wait(p.bar, 6, abort_);
-  const int cols = 32 * kFewWarps, blocks = (p.d + cols - 1) / cols;
+  few_arrive<FEW_WORK>(p.bar, 6);
+  few_wait<FEW_WORK>(p.bar, 6, abort_);
+  const int blocks = (p.d + kFewWork - 1) / kFewWork;
   for (int unit = blockIdx.x; unit < T * blocks; unit += gridDim.x) {
-    const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
+    const int t = unit / blocks, c = (unit - t * blocks) * kFewWork + tid;
     float q = 0.0f;
-    for (int j = tid; j < p.d / 16; j += 32 * kFewWarps)
+    for (int j = tid; j < p.d / 16; j += kFewWork)
       q += __ldcg(&p.bss[static_cast<size_t>(t) * (p.d / 16) + j]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-    if (lane == 0) tb.red[warp][0] = q;
-    few_bar();
+    if (lane == 0) tb.red[warp] = q;
+    few_bar<FEW_WORK>();
     q = 0.0f;
-    for (int w = 0; w < kFewWarps; ++w) q += tb.red[w][0];
+    for (int w = 0; w < kFewMmaWarps + kFewEpiWarps; ++w) q += tb.red[w];
     const float inv = 1.0f / sqrtf(q / p.d + p.eps_block);
     if (c < p.d) resid_out(t, c, __ldcg(&p.b[static_cast<size_t>(t) * p.d + c]) * inv);
-    few_bar();
+    few_bar<FEW_WORK>();
   }
 }
 

@@ -954,12 +954,10 @@ moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, con
 // ------------------------------------------------------------------ the layer for a few tokens
 
 constexpr int kFewSmem = 232448 - 4096;  // dynamic shared memory: 227 KB less the static tables
-constexpr int kFewMinStages = 3;
-
 // Shared-memory layout and workspace of moe_layer_forward_few; stages == 0: it does not fit.
 struct FewLayout {
-  size_t bar, logits, z, a, s, ss, y, v_down, v_up, b, bss, total;
-  int act_bytes, stages, smem;
+  size_t bar, logits, z, zss, a, s, ss, y, v_down, v_up, b, bss, total;
+  int pool_bytes, stages, turns, resident, smem;
 };
 FewLayout few_layout(const moe_config_t& c, int rank) {
   FewLayout L{};
@@ -969,6 +967,7 @@ FewLayout few_layout(const moe_config_t& c, int rank) {
   L.bar = take(kFewBarriers * 64);
   L.logits = take(T * c.n_experts * 4);
   L.z = take(c.d_latent > 0 ? T * E * 4 : 0);
+  L.zss = take(c.pre_norm ? T * (E / 16) * 4 : 0);
   L.a = take(TK * H * 4);
   L.s = take(TK * E * 4);
   L.ss = take(c.expert_norm ? TK * (E / 16) * 4 : 0);
@@ -978,19 +977,25 @@ FewLayout few_layout(const moe_config_t& c, int rank) {
   L.b = take(c.post_norm ? T * d * 4 : 0);
   L.bss = take(c.post_norm ? T * (d / 16) * 4 : 0);
   L.total = o;
-  size_t act;
-  if (c.dtype == MOE_F32) {
-    act = T * (std::max(d, H) * 4 + 16);
-  } else {
-    act = std::max(T * (d * 2 + 64), 2 * T * (H * 2 + 64));
-    if (c.d_latent > 0) act = std::max(act, 2 * T * (E * 2 + 64));
-  }
-  act = align_up(act, 128);
-  const size_t rest = 2 * kFewRedFloats * 4 + align_up(T * rank * 4, 16);
-  if (act + rest + kFewMinStages * kFewStageBytes > static_cast<size_t>(kFewSmem)) return L;
-  L.act_bytes = static_cast<int>(act);
-  L.stages = std::min<int>(kFewMaxStages, static_cast<int>((kFewSmem - act - rest) / kFewStageBytes));
-  L.smem = static_cast<int>(act + rest) + L.stages * kFewStageBytes;
+  const bool f32 = c.dtype == MOE_F32;
+  const size_t planes = f32 ? 1 : 2;  // hi and lo
+  auto row = [&](size_t K) { return static_cast<size_t>(few_row_pitch(f32, static_cast<int>(K))); };
+  // dense stages: u (and y) of every token; without latent projections u stays through the experts
+  size_t dense = T * row(d);
+  if (c.d_latent > 0) dense = std::max(dense, planes * T * row(E));
+  const size_t expert = planes * T * std::max(row(E), row(H));  // if one expert has every token
+  const size_t rest = 1024 + kFewRedBufs * kFewRedFloats * 4 + align_up(T * rank * 4, 16);  // 1024: alignment
+  if (std::max(dense, expert) + rest > static_cast<size_t>(kFewSmem)) return L;
+  L.pool_bytes = static_cast<int>((kFewSmem - rest) / 1024 * 1024);
+  int st, tu;
+  few_ring(L.pool_bytes - static_cast<int>(expert), &st, &tu);
+  if (st == 0) return L;
+  // every token's z stays in shared memory through the first expert stage where that leaves the ring
+  // its full depth
+  L.resident = st == kFewMaxStages ? 1 : 0;
+  const size_t held = c.d_latent > 0 ? dense : std::max(dense, planes * T * row(H));
+  few_ring(L.pool_bytes - static_cast<int>(held), &L.stages, &L.turns);
+  L.smem = static_cast<int>(rest) + L.pool_bytes;
   return L;
 }
 
@@ -999,14 +1004,42 @@ moe_status_t check_few(const moe_config_t* cfg, const moe_adapters_t* ad, FewLay
   if (s != MOE_OK) return s;
   const moe_config_t& c = *cfg;
   if (c.T > kFewTokens) return MOE_ERR_UNSUPPORTED;
-  const int m = c.dtype == MOE_BF16 ? 64 : 16;
+  const int m = c.dtype == MOE_BF16 ? 64 : 32;
   if (c.d_model % m || c.d_ff % m) return MOE_ERR_UNSUPPORTED;
   *L = few_layout(c, ad ? std::max(ad->rank, 0) : 0);
   return c.T > 0 && L->stages == 0 ? MOE_ERR_UNSUPPORTED : MOE_OK;
 }
 
+// One weight matrix of `rows` rows (per half) of K values as the few-token kernel's TMA boxes: 16 rows,
+// or 8 rows of each of two halves, by kFewBlocks blocks of 128 bytes.
+bool make_few_map(CUtensorMap* m, const void* base, bool f32, uint64_t rows, uint64_t halves, uint64_t K,
+                  bool paired) {
+  auto fn = encode_fn();
+  if (!fn) return false;
+  const uint64_t es = f32 ? 4 : 2;
+  const cuuint64_t dims[4] = {128 / es, rows, halves, K * es / 128};
+  const cuuint64_t strides[3] = {K * es, rows * K * es, 128};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(128 / es), paired ? 8u : 16u, paired ? 2u : 1u,
+                             kFewBlocks};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(m, f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+            const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <bool kF32>
 moe_status_t launch_few(const FewParams& p, int smem, cudaStream_t st) {
+  FewMaps m{};
+  const uint64_t n = p.n, d = p.d, L = p.L, E = p.E, H = p.H, R = static_cast<uint64_t>(p.nA) * p.rank;
+  bool ok = make_few_map(&m.router, p.w_router, kF32, n, 1, d * p.wk_seg, false) &&
+            make_few_map(&m.gate_up, p.w_gu, kF32, p.swiglu ? H : n * H, p.swiglu ? 2 * n : 1, E, p.swiglu) &&
+            make_few_map(&m.w_down, p.w_down, kF32, n * E, 1, H, false);
+  if (L) ok = ok && make_few_map(&m.p_down, p.p_down, kF32, L, 1, d, false) &&
+              make_few_map(&m.p_up, p.p_up, kF32, d, 1, L, false);
+  if (R) ok = ok && make_few_map(&m.ad_down, p.down_a, kF32, R, 1, d, false) &&
+              make_few_map(&m.ad_up, p.up_a, kF32, R, 1, L, false);
+  if (!ok) return MOE_ERR_CUDA;
   auto kern = few_layer_kernel<kF32>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -1016,22 +1049,24 @@ moe_status_t launch_few(const FewParams& p, int smem, cudaStream_t st) {
   if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
   const int sms = device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
-  if (cudaMemsetAsync(p.bar, 0, kFewBarriers * 64, st) != cudaSuccess) return MOE_ERR_CUDA;
+  launch_k(few_init_kernel, 1, 128, 0, st, p.bar);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = static_cast<unsigned>(sms);
   cfg.blockDim = kFewThreads;
   cfg.dynamicSmemBytes = static_cast<size_t>(smem);
   cfg.stream = st;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeCooperative;
   attr[0].val.cooperative = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, kern, p) != cudaSuccess) {
+  cfg.numAttrs = 2;
+  if (cudaLaunchKernelEx(&cfg, kern, p, m) != cudaSuccess) {
     cudaGetLastError();
     return MOE_ERR_CUDA;
   }
-  return last_launch();
+  return last_launch(2);
 }
 
 // Host-side checks of a whole-layer forward (nothing is launched when they fail).  T == 0 passes.
@@ -1523,6 +1558,7 @@ moe_status_t moe_layer_forward_few(const moe_config_t* cfg, const moe_weights_t*
   p.bar = at<unsigned>(workspace, L.bar);
   p.logits = at<float>(workspace, L.logits);
   p.z = at<float>(workspace, L.z);
+  p.zss = at<float>(workspace, L.zss);
   p.a = at<float>(workspace, L.a);
   p.s = at<float>(workspace, L.s);
   p.ss = at<float>(workspace, L.ss);
@@ -1531,8 +1567,10 @@ moe_status_t moe_layer_forward_few(const moe_config_t* cfg, const moe_weights_t*
   p.v_up = at<float>(workspace, L.v_up);
   p.b = at<float>(workspace, L.b);
   p.bss = at<float>(workspace, L.bss);
+  p.pool_bytes = L.pool_bytes;
   p.stages = L.stages;
-  p.act_bytes = L.act_bytes;
+  p.turns = L.turns;
+  p.resident = L.resident;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return c.dtype == MOE_F32 ? launch_few<true>(p, L.smem, st) : launch_few<false>(p, L.smem, st);
 }

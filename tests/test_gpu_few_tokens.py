@@ -70,7 +70,7 @@ CASES = [
     dict(MUSE, T=8, d=2560, L=1536, I=1088, n=12, k=3),
     dict(SHAZ, T=1), dict(SHAZ, T=8, norm=1), dict(SHAZ, T=5, act="swiglu"), dict(SHAZ, T=4, d=512, I=1024, n=256),
     dict(SHAZ, T=3, dtype="f32", d=64, I=128, n=8, k=2), dict(SHAZ, T=8, dtype="f32", norm=1, act="swiglu"),
-    dict(SHAZ, T=2, dtype="f32", d=48, I=80, n=5, k=5, gate="sigmoid"),
+    dict(SHAZ, T=2, dtype="f32", d=96, I=160, n=5, k=5, gate="sigmoid"),
 ]
 
 

@@ -82,7 +82,7 @@ struct FewParams {
   float* w_out;                 // optional
   // workspace
   unsigned* bar;                // [kFewBarriers * 16], zeroed before the launch
-  float* logits;                // [T, n] pre-activation
+  float* logits;                // [T, kMaxExperts] u W_g^T
   float* z;                     // [T, L]
   float* zss;                   // [T, L/16] partial sums of squares of z (pre_norm)
   float* a;                     // [T*k, H]
@@ -95,6 +95,7 @@ struct FewParams {
   float* bss;                   // [T, d/16] (post_norm)
   int pool_bytes;               // ring and activations together
   int stages, turns;            // ring of the dense stages (few_ring)
+  int8_t ring_stages[kFewTokens + 1], ring_turns[kFewTokens + 1];  // and of the expert stages, by rows held
   int resident;                 // 1: the expert stages keep every token's z in shared memory
 };
 
@@ -422,47 +423,57 @@ __device__ __forceinline__ void few_chunk_f32(uint32_t stage, int kw, uint32_t x
 
 // Top-k of token t by one warp, into the tables (and CTA 0's copies to the caller's buffers); the
 // rules are those of moe_route: descending keys, ties to the lower index, a NaN key below every
-// other and latched.
+// other and latched.  Lane l looks at experts 8 l .. 8 l + 7.  This code runs once per call, so its
+// rounds stay a loop: unrolled, fetching the instructions took longer than executing them.
 __device__ __forceinline__ void few_topk(const FewParams& p, FewTables& tb, int t, int lane) {
-  uint32_t key[kMaxExperts / 32];
-  float pay[kMaxExperts / 32];
+  constexpr int kPer = kMaxExperts / 32;
+  static_assert(kPer == 8, "two 16-byte loads a lane");
+  const bool sig = p.gate_mode == MOE_GATE_SIGMOID;
+  const float4* row = reinterpret_cast<const float4*>(p.logits + static_cast<size_t>(t) * kMaxExperts);
+  float4 lo = make_float4(0, 0, 0, 0), hi = lo;
+  if (lane * kPer < p.n) {
+    lo = __ldcg(row + lane * 2);
+    hi = __ldcg(row + lane * 2 + 1);
+  }
+  float pay[kPer] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  uint32_t key[kPer];
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kMaxExperts / 32; ++i) {
-    const int e = lane + 32 * i;
+  for (int i = 0; i < kPer; ++i) {
+    const int e = lane * kPer + i;
     key[i] = 0u;
-    pay[i] = 0.0f;
     if (e < p.n) {
-      float l = __ldcg(&p.logits[static_cast<size_t>(t) * p.n + e]);
+      float l = pay[i];
+      if (sig) l *= p.logit_mult;
+      if (p.logit_bias) l += p.logit_bias[e];
       float kf = l;
-      if (p.gate_mode == MOE_GATE_SIGMOID) {
+      if (sig) {
         l = 1.0f / (1.0f + expf(-l));
         kf = l + (p.sel_bias ? p.sel_bias[e] : 0.0f);
       }
       if (p.logits_out && blockIdx.x == 0) p.logits_out[static_cast<size_t>(t) * p.n + e] = l;
-      pay[i] = l;
       if (kf != kf) {
         bad = true;
         kf = -INFINITY;
-        pay[i] = p.gate_mode == MOE_GATE_SIGMOID ? 0.0f : -INFINITY;
+        l = sig ? 0.0f : -INFINITY;
       }
+      pay[i] = l;
       key[i] = ordered_key(kf);
     }
   }
   float mine = 0.0f, first = 0.0f;  // lane j: the j-th selected value
-#pragma unroll
-  for (int j = 0; j < kMaxTopK; ++j) {
-    if (j >= p.k) continue;
-    uint32_t bk = 0u;
+#pragma unroll 1
+  for (int j = 0; j < p.k; ++j) {
+    uint32_t bk = 0u;  // this lane's best candidate (the lowest index among equal keys)
     int bi = 0x7fffffff;
     float bp = 0.0f;
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (key[i] > bk) { bk = key[i]; bi = lane + 32 * i; bp = pay[i]; }
+    for (int i = 0; i < kPer; ++i)
+      if (key[i] > bk) { bk = key[i]; bi = lane * kPer + i; bp = pay[i]; }
     const uint32_t m = __reduce_max_sync(0xffffffffu, bk);
     const uint32_t win =
         __reduce_min_sync(0xffffffffu, bk == m ? static_cast<uint32_t>(bi) : 0xffffffffu);
-    const float s = __shfl_sync(0xffffffffu, bp, static_cast<int>(win & 31u));
+    const float s = __shfl_sync(0xffffffffu, bp, static_cast<int>(win / kPer & 31u));
     if (j == 0) first = s;
     if (lane == j) {
       mine = s;
@@ -470,13 +481,12 @@ __device__ __forceinline__ void few_topk(const FewParams& p, FewTables& tb, int 
       tb.idx[t * p.k + j] = min(static_cast<int>(win), p.n - 1);
     }
 #pragma unroll
-    for (int i = 0; i < kMaxExperts / 32; ++i)
-      if (static_cast<uint32_t>(lane + 32 * i) == win) key[i] = 0u;
+    for (int i = 0; i < kPer; ++i)
+      if (static_cast<uint32_t>(lane * kPer + i) == win) key[i] = 0u;
   }
   bad = __any_sync(0xffffffffu, bad);
   if (lane == 0 && blockIdx.x == 0 && (bad || !(fabsf(first) <= 3.0e38f)))
     latch_status(MOE_ERR_DEVICE_CHECK);
-  const bool sig = p.gate_mode == MOE_GATE_SIGMOID;
   const float ex = lane < p.k ? (sig ? mine : expf(mine - first)) : 0.0f;
   float sum = ex;
 #pragma unroll
@@ -493,9 +503,8 @@ __device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, vol
   // distinct experts in ascending order, each with its slots in token order (thread = expert)
   const int slots = p.T * p.k, tid = warp * 32 + lane;
   unsigned long long hits = 0;  // slots routed to this thread's expert
-#pragma unroll 4
-  for (int s = 0; s < kFewSlots; s += 4) {
-    if (s >= slots) break;
+#pragma unroll 1
+  for (int s = 0; s < slots; s += 4) {
     const int4 v = *reinterpret_cast<const int4*>(&tb.idx[s]);  // entries past the last slot: masked
     const unsigned f = (v.x == tid) | (v.y == tid) << 1 | (v.z == tid) << 2 | (v.w == tid) << 3;
     hits |= static_cast<unsigned long long>(f) << s;
@@ -527,14 +536,9 @@ __device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, vol
   if (tid == 0) {
     tb.dist = total;
     tb.rows = p.resident ? p.T : rows;
-    if (p.L) {
-      const int pitch = max(few_row_pitch(false, p.E), few_row_pitch(false, p.H));
-      few_ring(p.pool_bytes - 2 * tb.rows * pitch, &tb.stages, &tb.turns);
-    } else {  // the first expert stage reads u where the router left it
-      tb.rows = p.T;
-      tb.stages = p.stages;
-      tb.turns = p.turns;
-    }
+    if (!p.L) tb.rows = p.T;  // the first expert stage reads u where the router left it
+    tb.stages = p.ring_stages[tb.rows];
+    tb.turns = p.ring_turns[tb.rows];
   }
   if (blockIdx.x == 0 && tid < slots) {
     if (p.idx_out) p.idx_out[tid] = tb.idx[tid];
@@ -812,6 +816,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int cols = kFewMma, blocks = (p.E + cols - 1) / cols;
       for (int unit = blockIdx.x; unit < T * blocks; unit += gridDim.x) {
         const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
+        float s[kMaxTopK];  // in flight while the norms are summed
+#pragma unroll
+        for (int j = 0; j < kMaxTopK; ++j)
+          s[j] = mma && c < p.E && j < k ? __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) : 0.0f;
         if (warp < k) {
           float inv = 1.0f;
           if (p.expert_norm) {
@@ -827,9 +835,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         few_bar<FEW_WORK>();
         if (mma && c < p.E) {
           float y = 0.0f;
-          for (int j = 0; j < k; ++j)
-            y = fmaf(tb.w[t * k + j],
-                     __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) * tb.inv[j], y);
+#pragma unroll
+          for (int j = 0; j < kMaxTopK; ++j)
+            if (j < k) y = fmaf(tb.w[t * k + j], s[j] * tb.inv[j], y);
           if (p.L) p.y[static_cast<size_t>(t) * p.E + c] = y;
           else if (kF32) static_cast<float*>(p.out)[static_cast<size_t>(t) * p.E + c] = y;
           else static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.E + c] = f32_to_bf16(y);
@@ -978,10 +986,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const bool mine = col < m;
       switch (t.kind) {
         case FEW_ROUTER:
-          if (mine && f < p.n) {
-            if (p.gate_mode == MOE_GATE_SIGMOID) v *= p.logit_mult;
-            p.logits[static_cast<size_t>(col) * p.n + f] = v + (p.logit_bias ? p.logit_bias[f] : 0.0f);
-          }
+          if (mine && f < p.n) p.logits[static_cast<size_t>(col) * kMaxExperts + f] = v;
           break;
         case FEW_AD_DOWN:
         case FEW_AD_UP:  // inner products scale * (A x), for the tokens that use this adapter

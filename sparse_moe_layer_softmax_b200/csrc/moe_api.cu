@@ -958,14 +958,16 @@ constexpr int kFewSmem = 232448 - 4096;  // dynamic shared memory: 227 KB less t
 struct FewLayout {
   size_t bar, logits, z, zss, a, s, ss, y, v_down, v_up, b, bss, total;
   int pool_bytes, stages, turns, resident, smem;
+  int ring_stages[kFewTokens + 1], ring_turns[kFewTokens + 1];  // expert stages, by rows held
 };
 FewLayout few_layout(const moe_config_t& c, int rank) {
   FewLayout L{};
+  if (c.T == 0) return L;
   const size_t T = c.T, TK = T * c.top_k, E = expert_in(c), H = c.d_ff, d = c.d_model;
   size_t o = 0;
   auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
   L.bar = take(kFewBarriers * 64);
-  L.logits = take(T * c.n_experts * 4);
+  L.logits = take(T * kMaxExperts * 4);
   L.z = take(c.d_latent > 0 ? T * E * 4 : 0);
   L.zss = take(c.pre_norm ? T * (E / 16) * 4 : 0);
   L.a = take(TK * H * 4);
@@ -987,14 +989,19 @@ FewLayout few_layout(const moe_config_t& c, int rank) {
   const size_t rest = 1024 + kFewRedBufs * kFewRedFloats * 4 + align_up(T * rank * 4, 16);  // 1024: alignment
   if (std::max(dense, expert) + rest > static_cast<size_t>(kFewSmem)) return L;
   L.pool_bytes = static_cast<int>((kFewSmem - rest) / 1024 * 1024);
-  int st, tu;
-  few_ring(L.pool_bytes - static_cast<int>(expert), &st, &tu);
-  if (st == 0) return L;
+  for (size_t rows = 1; rows <= T; ++rows)
+    few_ring(L.pool_bytes - static_cast<int>(planes * rows * std::max(row(E), row(H))), &L.ring_stages[rows],
+             &L.ring_turns[rows]);
+  if (L.ring_stages[T] == 0) return L;
   // every token's z stays in shared memory through the first expert stage where that leaves the ring
   // its full depth
-  L.resident = st == kFewMaxStages ? 1 : 0;
+  L.resident = L.ring_stages[T] == kFewMaxStages ? 1 : 0;
   const size_t held = c.d_latent > 0 ? dense : std::max(dense, planes * T * row(H));
   few_ring(L.pool_bytes - static_cast<int>(held), &L.stages, &L.turns);
+  if (c.d_latent == 0) {  // u keeps its place: the ring stays as it is
+    L.ring_stages[T] = L.stages;
+    L.ring_turns[T] = L.turns;
+  }
   L.smem = static_cast<int>(rest) + L.pool_bytes;
   return L;
 }
@@ -1571,6 +1578,10 @@ moe_status_t moe_layer_forward_few(const moe_config_t* cfg, const moe_weights_t*
   p.stages = L.stages;
   p.turns = L.turns;
   p.resident = L.resident;
+  for (int i = 0; i <= c.T; ++i) {
+    p.ring_stages[i] = static_cast<int8_t>(L.ring_stages[i]);
+    p.ring_turns[i] = static_cast<int8_t>(L.ring_turns[i]);
+  }
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   return c.dtype == MOE_F32 ? launch_few<true>(p, L.smem, st) : launch_few<false>(p, L.smem, st);
 }

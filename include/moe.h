@@ -325,6 +325,44 @@ MOE_API moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_w
                                             float* topk_w_out, const moe_layer_taps_t* taps,
                                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* The latent projections with the low-rank adapters of many requests at once: for every token t with
+ * a = token_adapter[t] (-1: none, else in [0, n_adapters); the tokens of an adapter may lie anywhere),
+ *   down: z_raw[t] = dtype(u_t P_down^T + scale[a] B_a (A_a u_t));
+ *   up:   b_t = dtype(y_t P_up^T + scale[a] B_a (A_a y_t)), then the residual update of moe_latent_up.
+ * Sums are fp32.  In batches whose reduction is not split (more than 64 tokens, or a width that is no
+ * multiple of 128) scale[a] A_a x is rounded to bf16 on the way.  A token without an adapter gets the
+ * bits of moe_latent_down / moe_latent_up.  bf16 only.
+ *   - token_adapter: [T] int32, aligned to 4 bytes (a slice of a longer array may be passed).  An index
+ *     outside [-1, n_adapters) latches MOE_ERR_DEVICE_CHECK and means none.
+ *   - Adapter weights must be finite.  One adapter's non-finite values never reach another's tokens:
+ *     with more than 64 tokens an adapter whose B holds one is left out (its tokens get the projection
+ *     alone) and MOE_ERR_DEVICE_CHECK is latched; otherwise they reach its own tokens' outputs.
+ *   - workspace: moe_adapters_workspace_size bytes (host arithmetic; grows with T * min(n_adapters,
+ *     256) * 128 bytes), contents need not be initialised.  Calls that share it must not overlap.
+ *   - Outputs must not alias inputs.  Errors as for moe_latent_down / moe_latent_up, and
+ *     MOE_ERR_UNSUPPORTED for a rank that is no multiple of 8 or above MOE_ADAPTER_MAX_RANK. */
+MOE_API moe_status_t moe_adapters_workspace_size(const moe_config_t* cfg,
+                                                 const moe_adapters_t* adapters, size_t* bytes);
+MOE_API moe_status_t moe_latent_down_adapters(const moe_config_t* cfg, const void* u,
+                                              const void* p_down, const moe_adapters_t* adapters,
+                                              const int32_t* token_adapter, void* z_raw,
+                                              void* workspace, size_t workspace_bytes, void* stream);
+MOE_API moe_status_t moe_latent_up_adapters(const moe_config_t* cfg, const void* y, const void* p_up,
+                                            const moe_adapters_t* adapters,
+                                            const int32_t* token_adapter, const void* r,
+                                            const float* resid_g, void* out, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/* moe_layer_forward with every token's adapter on both latent projections (the router reads u, so the
+ * adapters do not change the routing).  workspace: moe_workspace_size + moe_adapters_workspace_size
+ * bytes. */
+MOE_API moe_status_t moe_layer_forward_adapters(const moe_config_t* cfg, const moe_weights_t* w,
+                                                const moe_adapters_t* adapters,
+                                                const int32_t* token_adapter, const void* u,
+                                                const void* r, void* out, float* logits_out,
+                                                int32_t* topk_idx_out, float* topk_w_out,
+                                                void* workspace, size_t workspace_bytes, void* stream);
+
 /* The whole layer, as moe_layer_forward defines it, for 1 .. MOE_FEW_MAX_TOKENS tokens in one
  * persistent kernel (and one memset of its barrier counters): single-stream decoding, or the
  * verification of a few drafted tokens, where the launches of the batch path cost as much as the

@@ -32,7 +32,9 @@ EXPORTS = ("moe_status_string", "moe_workspace_size", "moe_route", "moe_permute"
            "moe_router_split_weights", "moe_residual_update", "moe_noisy_gate",
            "moe_noisy_gate_workspace_size", "moe_host_staging_size", "moe_layer_forward_host",
            "moe_row_sumsq_parts", "moe_gather_rows", "moe_layer_forward_taps",
-           "moe_dispatch_rows", "moe_few_workspace_size", "moe_layer_forward_few")
+           "moe_dispatch_rows", "moe_few_workspace_size", "moe_layer_forward_few",
+           "moe_adapters_workspace_size", "moe_latent_down_adapters", "moe_latent_up_adapters",
+           "moe_layer_forward_adapters")
 FEW_MAX_TOKENS = 8
 PROFILE_STAGES = ("route", "latent_down", "dispatch", "expert_gate_up", "expert_down", "combine",
                   "latent_up_resgate")
@@ -116,6 +118,10 @@ def lib():
             "moe_permute_static": [cp, vp, vp, vp, vp, vp, vp, vp, vp],
             "moe_dispatch_rows": [cp, vp, vp, vp, vp, vp],
             "moe_few_workspace_size": [cp, ap, ctypes.POINTER(sz)],
+            "moe_adapters_workspace_size": [cp, ap, ctypes.POINTER(sz)],
+            "moe_latent_down_adapters": [cp, vp, vp, ap, vp, vp, vp, sz, vp],
+            "moe_latent_up_adapters": [cp, vp, vp, ap, vp, vp, vp, vp, vp, sz, vp],
+            "moe_layer_forward_adapters": [cp, wp, ap, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_layer_forward_few": [cp, wp, ap, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
             "moe_selftest_wait_timeout": [ctypes.c_longlong, vp, vp],
         }
@@ -364,6 +370,49 @@ def _check_adapter_shapes(cfg, adapters, token_adapter, pairs):
                              f"{want[1]}")
 
 
+def adapters_workspace_size(cfg: Config, adapters: Adapters) -> int:
+    """Workspace bytes of the adapted projections (a layer forward adds workspace_size(cfg))."""
+    n = ctypes.c_size_t()
+    _check("moe_adapters_workspace_size", lib().moe_adapters_workspace_size(
+        ctypes.byref(cfg), ctypes.byref(adapters), ctypes.byref(n)))
+    return n.value
+
+
+def moe_latent_down_adapters(cfg, u, p_down, adapters, token_adapter, z_raw, workspace,
+                             workspace_bytes=0, stream=None):
+    """z_raw = u P_down^T plus each token's adapter (``adapters`` from make_adapters,
+    ``token_adapter`` [T] int32, -1: none)."""
+    _check_adapter_shapes(cfg, adapters, token_adapter, ("down",))
+    workspace_bytes = workspace_bytes or workspace.numel() * workspace.element_size()
+    _check("moe_latent_down_adapters", lib().moe_latent_down_adapters(
+        ctypes.byref(cfg), _ptr(u), _ptr(p_down), ctypes.byref(adapters), _ptr(token_adapter),
+        _ptr(z_raw), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_latent_up_adapters(cfg, y, p_up, adapters, token_adapter, r, resid_g, out, workspace,
+                           workspace_bytes=0, stream=None):
+    """out = residual update of y P_up^T plus each token's adapter."""
+    _check_adapter_shapes(cfg, adapters, token_adapter, ("up",))
+    workspace_bytes = workspace_bytes or workspace.numel() * workspace.element_size()
+    _check("moe_latent_up_adapters", lib().moe_latent_up_adapters(
+        ctypes.byref(cfg), _ptr(y), _ptr(p_up), ctypes.byref(adapters), _ptr(token_adapter), _ptr(r),
+        _ptr(resid_g), _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def moe_layer_forward_adapters(cfg, weights: Weights, adapters, token_adapter, u, r, out,
+                               logits_out=None, topk_idx_out=None, topk_w_out=None, workspace=None,
+                               workspace_bytes=0, stream=None):
+    """moe_layer_forward with each token's adapter on both latent projections; the workspace holds
+    workspace_size(cfg) + adapters_workspace_size(cfg, adapters) bytes."""
+    if workspace is not None and not workspace_bytes:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check_adapter_shapes(cfg, adapters, token_adapter, ("down", "up"))
+    _check("moe_layer_forward_adapters", lib().moe_layer_forward_adapters(
+        ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(adapters), _ptr(token_adapter), _ptr(u),
+        _ptr(r), _ptr(out), _ptr(logits_out), _ptr(topk_idx_out), _ptr(topk_w_out), _ptr(workspace),
+        workspace_bytes, _stream(stream)))
+
+
 def few_workspace_size(cfg: Config, adapters: Adapters | None = None) -> int:
     n = ctypes.c_size_t()
     _check("moe_few_workspace_size", lib().moe_few_workspace_size(
@@ -430,18 +479,29 @@ class MoELayer:
             self.weights = weights
         self._w = make_weights(weights)
         self.adapters = make_adapters(adapters) if adapters is not None else None
-        self.workspace = torch.empty(workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        need = workspace_size(cfg)
+        if self.adapters is not None:
+            need += adapters_workspace_size(cfg, self.adapters)
+        self.workspace = torch.empty(need, dtype=torch.uint8, device="cuda")
         self._few_workspace = None
 
     def forward(self, u, r=None, out=None, logits_out=None, topk_idx_out=None, topk_w_out=None,
-                stream=None, taps: dict | None = None):
+                stream=None, taps: dict | None = None, token_adapter=None):
         """One moe_layer_forward; with ``taps`` (a dict of device tensors under the keys z, s, y,
-        inv_perm) one moe_layer_forward_taps that also copies those intermediates."""
+        inv_perm) one moe_layer_forward_taps that also copies those intermediates; with
+        ``token_adapter`` ([T] int32, -1: none) one moe_layer_forward_adapters with the layer's
+        adapters."""
         import torch
         if out is None:
             out = torch.empty_like(u)
         r = r if r is not None else u
-        if taps is None:
+        if token_adapter is not None:
+            if self.adapters is None or taps is not None:
+                raise ValueError("token_adapter needs a layer with adapters, and takes no taps")
+            moe_layer_forward_adapters(self.cfg, self._w, self.adapters, token_adapter, u, r, out,
+                                       logits_out, topk_idx_out, topk_w_out, self.workspace,
+                                       stream=stream)
+        elif taps is None:
             moe_layer_forward(self.cfg, self._w, u, r, out, logits_out, topk_idx_out, topk_w_out,
                               self.workspace, stream=stream)
         else:

@@ -1,0 +1,337 @@
+// Low-rank adapters of many requests beside a dense projection: y_t = W x_t + s_a B_a (A_a x_t), where
+// a is token t's adapter (or none).
+//
+// The inner products v_t = s_a A_a x_t (rank values per token) are computed first, then the projection
+// adds B_a v_t:
+//   - Up to 64 rows (a decode batch) the weight stream of W sets the time.  The inner products run in
+//     their own small kernel, one CTA per (adapter, range of the reduction), while the projection
+//     kernel already streams W; its finishing warps add B_a v_t in fp32 on the CUDA cores, before the
+//     tile's sum is there (gemm_splitk.cuh).  Every token reads its own adapter only.
+//   - Larger batches put B_a v_t on the tensor cores: the projection GEMM's reduction is extended, tile
+//     by tile, by one 64-wide k-block per adapter that the tile's rows use.  The activation operand of
+//     that block is v_t for the rows of that adapter and zero for the others, the weight operand the
+//     tile's rows of B_a (TMA fills the columns past the rank with zeros).  A tile of one prompt pays
+//     64 columns on top of the 8192 of the Muse projection, under 1%; nothing is sorted or gathered.
+//     v is rounded to bf16 there (an MMA operand): its error is 2^-9 of the adapter's term, below the
+//     2^-9 of the whole that storing the result costs.
+//     An MMA multiplies zero rows too, and zero times infinity is NaN: so that one adapter's broken
+//     weights cannot reach the tokens of others, each used B is looked through once per call, and an
+//     adapter that holds a non-finite value is left out and reported.
+#pragma once
+
+#include "common.cuh"
+#include "few_tokens.cuh"
+#include "gemm_tc.cuh"
+
+namespace moe {
+
+constexpr int kAdSmallRows = 64;     // rows of the small path
+constexpr int kAdSmallSplits = 8;    // ranges of the reduction, each a CTA of four warps
+constexpr int kAdChunk = 128;        // token rows of a tile of the tensor-core inner products
+constexpr int kAdGroupCols = 256;    // rows of A that one pass over the tokens multiplies
+constexpr int kAdStages = 4;
+constexpr int kAdMaxSplits = 16;
+constexpr int kAdMaxChunk = 256;     // rows of the projection's largest tile
+constexpr int kAdStageBytes = kAdChunk * 128 + kAdGroupCols * 128;
+constexpr int kAdSmem = kAdStages * kAdStageBytes + 1024;
+
+// A token's adapter, -1 for none; an index outside [-1, n) is reported once and means none.
+__device__ __forceinline__ int adapter_of(const int32_t* which, int t, int n, bool report) {
+  const int a = which[t];
+  if (a >= -1 && a < n) return a;
+  if (report) latch_status(MOE_ERR_DEVICE_CHECK);
+  return -1;
+}
+
+// ------------------------------------------------------------------ inner products, at most 64 rows
+//
+// v[split, t, :] = scale[a] * (A_a x_t over this split's columns).  CTA (t, split, rank tile) works if t
+// is the first token of its adapter, for all tokens of that adapter: A is read once.  Operands go from
+// global memory straight into m16n8k16 fragments (16 rows of A on M, 8 tokens on N; the reduction
+// index is permuted the same way in both, so every fragment is one 16-byte load); the four warps'
+// sums meet in shared memory.  Latency is all there is to this kernel: one token of rank 16 reads 262 KB.
+__global__ void __launch_bounds__(128)
+    adapter_shrink_small_kernel(const uint16_t* __restrict__ x, int T, int K,
+                                const uint16_t* __restrict__ A, const float* __restrict__ scale,
+                                const int32_t* __restrict__ which, int n, int rank,
+                                float* __restrict__ v) {
+  __shared__ int s_list[kAdSmallRows];
+  __shared__ int s_m[2];
+  __shared__ float s_red[4][16][kAdSmallRows + 1];
+  pdl_wait();
+  pdl_launch_dependents();
+  const int t = blockIdx.x, split = blockIdx.y, r0 = blockIdx.z * 16;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int a = adapter_of(which, t, n, split == 0 && r0 == 0 && tid == 0);
+  const bool same = tid < T && which[tid] == a;
+  if (__syncthreads_or(a < 0 || (same && tid < t))) return;  // no adapter, or an earlier token's CTA does it
+  const unsigned mask = __ballot_sync(0xffffffffu, same);  // T <= 64: warps 0 and 1
+  if (warp < 2 && lane == 0) s_m[warp] = __popc(mask);
+  __syncthreads();
+  if (same) s_list[(warp ? s_m[0] : 0) + __popc(mask & ((1u << lane) - 1u))] = tid;
+  __syncthreads();
+  const int m = s_m[0] + s_m[1];
+
+  const int g = lane >> 2, q = lane & 3;
+  const int steps = K / 32, parts = kAdSmallSplits * 4, w = split * 4 + warp;
+  const int k_lo = static_cast<int>(static_cast<long>(w) * steps / parts);
+  const int k_hi = static_cast<int>(static_cast<long>(w + 1) * steps / parts);
+  const uint16_t* a0 = A + (static_cast<size_t>(a) * rank + min(r0 + g, rank - 1)) * K + q * 8;
+  const uint16_t* a1 = A + (static_cast<size_t>(a) * rank + min(r0 + g + 8, rank - 1)) * K + q * 8;
+  float acc[kAdSmallRows / 8][4] = {};
+#pragma unroll 4
+  for (int s = k_lo; s < k_hi; ++s) {
+    const uint4 p0 = __ldg(reinterpret_cast<const uint4*>(a0 + s * 32));
+    const uint4 p1 = __ldg(reinterpret_cast<const uint4*>(a1 + s * 32));
+#pragma unroll
+    for (int j = 0; j < kAdSmallRows / 8; ++j) {
+      if (j * 8 < m) {
+        uint4 b = make_uint4(0, 0, 0, 0);
+        if (j * 8 + g < m)
+          b = __ldg(reinterpret_cast<const uint4*>(x + static_cast<size_t>(s_list[j * 8 + g]) * K + s * 32 + q * 8));
+        few_mma(acc[j], p0.x, p1.x, p0.y, p1.y, b.x, b.y);
+        few_mma(acc[j], p0.z, p1.z, p0.w, p1.w, b.z, b.w);
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kAdSmallRows / 8; ++j) {
+    if (j * 8 < m) {
+      s_red[warp][g][j * 8 + 2 * q] = acc[j][0];
+      s_red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
+      s_red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
+      s_red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+    }
+  }
+  __syncthreads();
+  const float sc = scale[a];
+  for (int i = tid; i < 16 * m; i += 128) {
+    const int row = i & 15, c = i >> 4;
+    if (r0 + row < rank)
+      v[(static_cast<size_t>(split) * T + s_list[c]) * rank + r0 + row] =
+          sc * ((s_red[0][row][c] + s_red[1][row][c]) + (s_red[2][row][c] + s_red[3][row][c]));
+  }
+}
+
+// ------------------------------------------------------------------ inner products, larger batches
+
+// The distinct adapters among `rows` (<= blockDim.x, <= 256) entries of s_ad, in order of first
+// appearance (negative entries have none): writes each row's slot to s_slot (-1: none) and the slots'
+// adapters to s_list; returns their number.  All threads of the CTA call it; s_cnt: 9 ints.
+__device__ __forceinline__ int adapter_slots(const int* s_ad, int rows, int* s_slot, int* s_list,
+                                             int* s_cnt) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int first = -1;  // first row with this row's adapter
+  if (tid < rows && s_ad[tid] >= 0) {
+    const int a = s_ad[tid];
+    for (first = 0; s_ad[first] != a; ++first) {}
+  }
+  const unsigned lead = __ballot_sync(0xffffffffu, first == tid);
+  if (lane == 0 && warp < 8) s_cnt[warp] = __popc(lead);
+  __syncthreads();
+  const int warps = min(8, static_cast<int>(blockDim.x) >> 5);
+  int before = 0, total = 0;
+  for (int w = 0; w < warps; ++w) {
+    before += w < warp ? s_cnt[w] : 0;
+    total += s_cnt[w];
+  }
+  if (first == tid) {
+    const int slot = before + __popc(lead & ((1u << lane) - 1u));
+    s_slot[tid] = slot;
+    s_list[slot] = s_ad[tid];
+  }
+  __syncthreads();
+  int slot = -1;
+  if (first >= 0) slot = s_slot[first];
+  __syncthreads();
+  if (tid < rows) s_slot[tid] = slot;
+  __syncthreads();
+  return total;
+}
+
+// v[split, t, :] = A_a x_t over this split's k-blocks, on the tensor cores: CTA (row chunk, split)
+// multiplies 128 token rows by the A rows of the adapters they use, up to 256 rows of A at a time,
+// and every token keeps its own adapter's columns.  Reading x sets the time (268 MB at prefill).  CTAs
+// past the chunks look through one adapter's B each: bad[a] = 1 if a used B holds a non-finite value.
+__global__ void __launch_bounds__(kGemmThreads, 1)
+    adapter_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
+                          int T, int K, const int32_t* __restrict__ which, int n, int rank, int chunks,
+                          const uint16_t* __restrict__ B, long b_elems, int* __restrict__ bad,
+                          float* __restrict__ v) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kAdStages], empty[kAdStages], tfull[2], tempty[2];
+  __shared__ uint32_t tmem_slot;
+  __shared__ int s_ad[kAdChunk], s_slot[kAdChunk], s_list[kAdChunk], s_cnt[9];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  if (static_cast<int>(blockIdx.x) >= chunks) {
+    pdl_wait();
+    pdl_launch_dependents();
+    if (blockIdx.y > 0) return;
+    const int a = static_cast<int>(blockIdx.x) - chunks;
+    bool used = false;
+    for (int t = tid; t < T; t += kGemmThreads) used = used || which[t] == a;
+    int found = 0;
+    if (__syncthreads_or(used)) {
+      const uint4* p = reinterpret_cast<const uint4*>(B + static_cast<size_t>(a) * b_elems);
+      for (long i = tid; i < b_elems / 8; i += kGemmThreads) {
+        const uint4 q = __ldg(p + i);
+        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)  // an exponent of all ones
+          if ((w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u) found = 1;
+      }
+    }
+    found = __syncthreads_or(found);
+    if (tid == 0) {
+      bad[a] = found;
+      if (found) latch_status(MOE_ERR_DEVICE_CHECK);
+    }
+    return;
+  }
+
+  uint8_t* tiles = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
+  const int row0 = static_cast<int>(blockIdx.x) * kAdChunk, rows = min(kAdChunk, T - row0);
+  const int KB = K / 64, splits = static_cast<int>(gridDim.y);
+  const int kb0 = static_cast<int>(blockIdx.y) * KB / splits, kb1 = (static_cast<int>(blockIdx.y) + 1) * KB / splits;
+  if (tid == 32) {
+    for (int s = 0; s < kAdStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
+    for (int b = 0; b < 2; ++b) { mbar_init(&tfull[b], 1); mbar_init(&tempty[b], 128); }
+    fence_barrier_init();
+  }
+  if (warp == 1) tmem_alloc(&tmem_slot, 512);
+  if (tid == 0) { tma_prefetch_desc(&tmX); tma_prefetch_desc(&tmA); }
+  pdl_wait();
+  pdl_launch_dependents();
+  if (tid < kAdChunk) s_ad[tid] = tid < rows ? adapter_of(which, row0 + tid, n, blockIdx.y == 0) : -1;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const int nslots = adapter_slots(s_ad, rows, s_slot, s_list, s_cnt);
+  const uint32_t tmem = tmem_slot;
+  // (the accumulator is read 16 columns at a time: a rank of 8 mod 16 stays clear of its end)
+  const int per = (rank % 16 ? kAdGroupCols - 16 : kAdGroupCols) / rank;
+  const int groups = (nslots + per - 1) / per;
+
+  if (warp == 0 && lane == 0) {
+    uint32_t stage = 0, phase = 0, issued = 0, parities = 0;
+    bool ok = true;
+    for (int gr = 0; gr < groups && ok; ++gr) {
+      const int s0 = gr * per, ns = min(per, nslots - s0);
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+        uint8_t* sa = tiles + stage * kAdStageBytes;
+        mbar_arrive_expect_tx(&full[stage], static_cast<uint32_t>(kAdChunk * 128 + ns * rank * 128));
+        tma_load_2d(&tmX, &full[stage], sa, kb * 64, row0);
+        for (int j = 0; j < ns; ++j)
+          tma_load_2d(&tmA, &full[stage], sa + kAdChunk * 128 + j * rank * 128, kb * 64, s_list[s0 + j] * rank);
+        issued |= 1u << stage;
+        parities = (parities & ~(1u << stage)) | (phase << stage);
+        if (++stage == kAdStages) { stage = 0; phase ^= 1; }
+      }
+    }
+    // No copy may still be landing in shared memory when the CTA exits.
+    for (int s = 0; s < kAdStages; ++s)
+      if (issued >> s & 1) mbar_wait(&full[s], parities >> s & 1);
+  } else if (warp == 1 && lane == 0) {
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int gr = 0; gr < groups && ok; ++gr) {
+      const int ns = min(per, nslots - gr * per), cols = (ns * rank + 15) / 16 * 16;
+      const int acc = gr & 1;
+      if (!mbar_wait(&tempty[acc], (gr >> 1 & 1) ^ 1)) break;
+      tc_fence_after();
+      for (int kb = kb0; kb < kb1; ++kb) {
+        if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
+        tc_fence_after();
+        const uint32_t a = smem_u32(tiles + stage * kAdStageBytes), b = a + kAdChunk * 128;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          tc_mma_bf16(tmem + acc * 256, smem_desc_k128(a + 32 * k), smem_desc_k128(b + 32 * k),
+                      idesc_bf16_f32(128, cols), (kb > kb0 || k > 0) ? 1u : 0u);
+        tc_commit(&empty[stage]);
+        if (++stage == kAdStages) { stage = 0; phase ^= 1; }
+      }
+      tc_commit(&tfull[acc]);  // also after a wait ran out: everything issued has finished
+      mbar_wait(&tfull[acc], gr >> 1 & 1);
+    }
+  } else if (warp >= 2) {
+    const int q = warp & 3, row = q * 32 + lane;
+    const int slot = row < rows ? s_slot[row] : -1;
+    float* dst = v + (static_cast<size_t>(blockIdx.y) * T + row0 + row) * rank;
+    for (int gr = 0; gr < groups; ++gr) {
+      const int s0 = gr * per, ns = min(per, nslots - s0), acc = gr & 1;
+      if (!epilogue_all(mbar_wait(&tfull[acc], gr >> 1 & 1))) break;
+      tc_fence_after();
+      for (int j = 0; j < ns; ++j) {
+        const bool mine = slot == s0 + j;
+        if (!__ballot_sync(0xffffffffu, mine)) continue;  // none of this warp's rows
+        for (int c = 0; c < rank; c += 16) {
+          float f[16];
+          tmem_ld16(tmem + (static_cast<uint32_t>(q * 32) << 16) + acc * 256 + j * rank + c, f);
+          if (mine) {
+            float4* d = reinterpret_cast<float4*>(dst + c);
+            d[0] = make_float4(f[0], f[1], f[2], f[3]);
+            d[1] = make_float4(f[4], f[5], f[6], f[7]);
+            if (c + 16 <= rank) {
+              d[2] = make_float4(f[8], f[9], f[10], f[11]);
+              d[3] = make_float4(f[12], f[13], f[14], f[15]);
+            }
+          }
+        }
+      }
+      tc_fence_before();
+      mbar_arrive(&tempty[acc]);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// The projection GEMM's operands of one row tile (CTA = tile of CH <= 256 rows): the adapters its rows
+// use (without the bad ones) and, per row, one block of rb * 64 columns for each of them: scale * v
+// (the splits added in order) in its own adapter's block, zeros in the others.
+__global__ void __launch_bounds__(kAdMaxChunk)
+    adapter_pack_kernel(const float* __restrict__ v, int splits, int T, const int32_t* __restrict__ which,
+                        int n, int rank, const float* __restrict__ scale, const int* __restrict__ bad,
+                        int CH, int cap, int rb, int* __restrict__ count, int* __restrict__ list,
+                        uint16_t* __restrict__ V) {
+  __shared__ int s_ad[kAdMaxChunk], s_slot[kAdMaxChunk], s_list[kAdMaxChunk], s_cnt[9];
+  // The projection may start: it multiplies x by W before it waits for this kernel.
+  pdl_launch_dependents();
+  pdl_wait();
+  const int tid = threadIdx.x, row0 = static_cast<int>(blockIdx.x) * CH, rows = min(CH, T - row0);
+  int a = tid < rows ? adapter_of(which, row0 + tid, n, false) : -1;
+  if (a >= 0 && bad[a]) a = -1;
+  s_ad[tid] = a;
+  __syncthreads();
+  const int ns = adapter_slots(s_ad, rows, s_slot, s_list, s_cnt);
+  if (tid == 0) count[blockIdx.x] = ns;
+  for (int i = tid; i < ns; i += kAdMaxChunk) list[static_cast<size_t>(blockIdx.x) * cap + i] = s_list[i];
+  const int vec = ns * rb * 8;  // 16-byte units of a row
+  const size_t pitch = static_cast<size_t>(cap) * rb * 64;
+  for (int i = tid; i < rows * vec; i += kAdMaxChunk) {
+    const int row = i / vec, u = i - row * vec, c = u % (rb * 8) * 8;
+    uint4 o = make_uint4(0, 0, 0, 0);
+    if (u / (rb * 8) == s_slot[row] && c < rank) {
+      float f[8] = {};
+      for (int s = 0; s < splits; ++s) {
+        const float4* p = reinterpret_cast<const float4*>(v + (static_cast<size_t>(s) * T + row0 + row) * rank + c);
+        const float4 x = __ldcg(p), y = __ldcg(p + 1);
+        f[0] += x.x; f[1] += x.y; f[2] += x.z; f[3] += x.w;
+        f[4] += y.x; f[5] += y.y; f[6] += y.z; f[7] += y.w;
+      }
+      const float sc = scale[s_ad[row]];
+      o = make_uint4(pack_bf16x2(sc * f[0], sc * f[1]), pack_bf16x2(sc * f[2], sc * f[3]),
+                     pack_bf16x2(sc * f[4], sc * f[5]), pack_bf16x2(sc * f[6], sc * f[7]));
+    }
+    *reinterpret_cast<uint4*>(V + (row0 + row) * pitch + u * 8) = o;
+  }
+}
+
+}  // namespace moe

@@ -45,15 +45,73 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
   return v;
 }
 
+// Low-rank adapters of the batch's rows: row t adds B_a v_t, a = which[t], v_t the sum of the `splits`
+// partial inner products v[s, t, :] (already scaled) that the kernel just before this one writes.
+struct SplitAdapt {
+  static constexpr bool kOn = true;
+  const float* v;          // [splits, rows, rank]
+  const uint16_t* b;       // [n, Nout, rank]
+  const int32_t* which;    // [rows]
+  int n, rank, splits;
+};
+constexpr int split_adapt_smem(int rank) { return kSplitBN * (rank + 4) * 4; }
+
+// The adapter terms of what splitk_reduce<., NS> finishes in this thread, in its order: kRows rows of 8
+// features each.  s_v: [kSplitBN][rank + 4] fp32, filled here by the 128 epilogue threads.  Runs while
+// the tile's weights stream in.
+template <int NS>
+__device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmParams& p, uint32_t rank,
+                                             int ft, float* s_v, float* add) {
+  constexpr int kFs = 128 / NS, kGroups = kFs / 8, kNr = 128 / kGroups, kRows = kSplitBN / kNr;
+  const int et = static_cast<int>(threadIdx.x) - 64, vp = ad.rank + 4;
+  for (int i = et; i < p.M * ad.rank; i += 128) {
+    const int t = i / ad.rank, c = i - t * ad.rank;
+    const int a = ad.which[t];
+    float x = 0.0f;
+    if (a >= 0 && a < ad.n)
+      for (int s = 0; s < ad.splits; ++s)
+        x += __ldcg(&ad.v[(static_cast<size_t>(s) * p.M + t) * ad.rank + c]);
+    s_v[t * vp + c] = x;
+  }
+  epilogue_bar();
+  const int g = et % kGroups, r0 = et / kGroups;
+  const int col = ft * 128 + static_cast<int>(rank) * kFs + g * 8;
+#pragma unroll
+  for (int q = 0; q < kRows; ++q) {
+    const int row = r0 + q * kNr;
+    float x[8] = {};
+    const int a = row < p.M ? ad.which[row] : -1;
+    if (a >= 0 && a < ad.n) {
+      const uint16_t* b = ad.b + (static_cast<size_t>(a) * p.Nout + col) * ad.rank;
+      for (int c = 0; c < ad.rank; c += 8) {
+        const float4 v0 = *reinterpret_cast<const float4*>(s_v + row * vp + c);
+        const float4 v1 = *reinterpret_cast<const float4*>(s_v + row * vp + c + 4);
+        const float v[8] = {v0.x, v0.y, v0.z, v0.w, v1.x, v1.y, v1.z, v1.w};
+        uint4 w[8];  // loaded together
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = __ldg(reinterpret_cast<const uint4*>(b + j * ad.rank + c));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint16_t* h = reinterpret_cast<const uint16_t*>(&w[j]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) x[j] = fmaf(bf16_to_f32(h[i]), v[i], x[j]);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) add[q * 8 + j] = x[j];
+  }
+}
+
 // Reduce + epilogue of one CTA of a cluster of NS: CTA `rank` finishes features
 // [rank * 128/NS, (rank + 1) * 128/NS) of feature tile `ft` for every row, in vectors of 8
 // features.  Thread (group g, row lane r) of the 128 epilogue threads takes features g*8 .. g*8+7
 // of that part and rows r, r + nr, ... (8/NS rows); all of its loads (the NS partial tiles through
 // distributed shared memory, the residual rows) are issued before the first sum, and the partials
 // are added in the order s = 0, 1, ..., NS-1.
-template <int kEpi, int NS>
+template <int kEpi, int NS, bool kAdd>
 __device__ __forceinline__ void splitk_reduce(const GemmParams& p, const float* part, uint32_t rank,
-                                              int ft) {
+                                              int ft, const float* add) {
   constexpr int kFs = 128 / NS, kGroups = kFs / 8, kNr = 128 / kGroups, kRows = kSplitBN / kNr;
   static_assert(kRows * kNr == kSplitBN && kGroups * 8 == kFs, "reduce layout");
   const int et = static_cast<int>(threadIdx.x) - 64;
@@ -117,6 +175,7 @@ __device__ __forceinline__ void splitk_reduce(const GemmParams& p, const float* 
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       float x = v[j];
+      if constexpr (kAdd) x += add[q * 8 + j];
       if constexpr (kEpi == EPI_RESGATE)
         x = __fmaf_rn(a[j], bf16_to_f32(rh[j]), __fmul_rn(b[j], round_bf16(x)));
       oh[j] = f32_to_bf16(x);
@@ -127,10 +186,11 @@ __device__ __forceinline__ void splitk_reduce(const GemmParams& p, const float* 
 
 // kEpi: EPI_STORE (out = dtype(sum)) or EPI_RESGATE (out = dtype(alpha r + beta dtype(sum))).
 // Grid: (Nout / 128) * S CTAs in clusters of S (2 <= S <= 8, S divides K / 64); rows p.M <= kSplitBN.
-template <int kEpi>
+template <int kEpi, class Adapt = NoAdapt>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_splitk_cluster_kernel(const __grid_constant__ CUtensorMap tmX,
-                               const __grid_constant__ CUtensorMap tmW, const GemmParams p) {
+                               const __grid_constant__ CUtensorMap tmW, const GemmParams p,
+                               const Adapt ad) {
   static_assert(kEpi == EPI_STORE || kEpi == EPI_RESGATE, "dense projection epilogues");
   using S = SplitShape;
   extern __shared__ uint8_t smem_raw[];
@@ -160,12 +220,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
-  pdl_wait();
+  // With adapters the kernel before this one only makes their inner products, and started once
+  // everything before it was complete: x may be read at once.
+  if (!Adapt::kOn) pdl_wait();
   pdl_launch_dependents();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
+  float add[Adapt::kOn ? 32 : 1];
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
@@ -210,6 +273,15 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   } else if (warp >= 2) {
     // ------------------------------------------------------------ partial tile to shared memory
     const int q = warp & 3;  // TMEM lane quarter: features 32q .. 32q + 31
+    if constexpr (Adapt::kOn) {
+      pdl_wait();
+      float* s_v = reinterpret_cast<float*>(tiles + kSplitStages * S::kStageBytes + 256);
+      switch (ns) {
+        case 2: splitk_adapt<2>(ad, p, rank, ft, s_v, add); break;
+        case 4: splitk_adapt<4>(ad, p, rank, ft, s_v, add); break;
+        default: splitk_adapt<8>(ad, p, rank, ft, s_v, add); break;
+      }
+    }
     mbar_wait(tfull, 0);
     tc_fence_after();
     const uint32_t tb = tmem_base + (static_cast<uint32_t>(q * 32) << 16);
@@ -229,9 +301,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   if (warp >= 2) {
     // ------------------------------------------------------------ reduce + epilogue
     switch (ns) {
-      case 2: splitk_reduce<kEpi, 2>(p, part, rank, ft); break;
-      case 4: splitk_reduce<kEpi, 4>(p, part, rank, ft); break;
-      default: splitk_reduce<kEpi, 8>(p, part, rank, ft); break;
+      case 2: splitk_reduce<kEpi, 2, Adapt::kOn>(p, part, rank, ft, add); break;
+      case 4: splitk_reduce<kEpi, 4, Adapt::kOn>(p, part, rank, ft, add); break;
+      default: splitk_reduce<kEpi, 8, Adapt::kOn>(p, part, rank, ft, add); break;
     }
   }
   __syncthreads();

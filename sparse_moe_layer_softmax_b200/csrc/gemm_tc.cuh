@@ -70,6 +70,23 @@ struct GemmParams {
   int tail_m64;              // 1: normal-orientation tiles of at most 64 rows run M = 64 MMAs
 };
 
+// Extension of a dense projection's reduction by low-rank adapters: row tile `chunk` multiplies, after
+// the K columns of X and W, count[chunk] * rblocks further blocks of 64: block (slot, rb) takes columns
+// (slot * rblocks + rb) * 64 of v's rows against columns rb * 64 of the tile's rows of adapter
+// list[chunk * cap + slot]'s matrix in b.  v, count and list come from the kernels just before this one,
+// which run on while X and W are multiplied: only the extension waits for them.
+struct NoAdapt {
+  static constexpr bool kOn = false;
+};
+struct GemmAdapt {
+  static constexpr bool kOn = true;
+  CUtensorMap v;     // [rows, cap * rblocks * 64]
+  CUtensorMap b;     // [n_adapters * Nout, rank]
+  const int* count;
+  const int* list;
+  int cap, rblocks;
+};
+
 // Shared memory that stages the bf16 output of the normal-orientation epilogues: one 4 KB
 // buffer (32 rows x 128 bytes) per epilogue warp.
 constexpr int kStageOutBytes = 4 * 4096;
@@ -434,10 +451,11 @@ __device__ __forceinline__ void epilogue_rows(const GemmParams& p, int row0, int
     }
 }
 
-template <bool kSwap, int BN, int kEpi, int kStages>
+template <bool kSwap, int BN, int kEpi, int kStages, class Adapt = NoAdapt>
 __global__ void __launch_bounds__(kGemmThreads, 1)
     gemm_tc_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
-                   const __grid_constant__ CUtensorMap tmO, const GemmParams p) {
+                   const __grid_constant__ CUtensorMap tmO, const GemmParams p,
+                   const __grid_constant__ Adapt ad) {
   using S = GemmShape<kSwap, BN, kEpi>;
   constexpr bool kStageOut = stages_output<kSwap, kEpi>();
   extern __shared__ uint8_t smem_raw[];
@@ -474,7 +492,9 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
-  pdl_wait();
+  // With adapters the kernels before this one only make the extension's operands, and started once
+  // everything before them was complete: X may be read at once.
+  if (!Adapt::kOn) pdl_wait();
   pdl_launch_dependents();  // one CTA per SM, all resident: the next kernel may launch
 
   // ---- group segments and the per-group tile prefix (warp 0)
@@ -560,6 +580,23 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         last_parity[stage] = phase;
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
+      if constexpr (Adapt::kOn) {
+        pdl_wait();
+        const int ext = ok ? __ldcg(&ad.count[c.chunk]) * ad.rblocks : 0;
+        for (int x = 0; x < ext; ++x) {
+          const int slot = x / ad.rblocks, rb = x - slot * ad.rblocks;
+          const int brow = __ldcg(&ad.list[static_cast<size_t>(c.chunk) * ad.cap + slot]) * p.Nw + c.ft * S::kFO;
+          if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+          uint8_t* sa = tiles + stage * S::kStageBytes;
+          uint8_t* sb = sa + S::kABytes;
+          mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
+          tma_load_2d(&ad.v, &full[stage], kSwap ? sb : sa, x * 64, c.row0);
+          tma_load_2d(&ad.b, &full[stage], kSwap ? sa : sb, rb * 64, brow);
+          issued[stage] = true;
+          last_parity[stage] = phase;
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
     }
     // No copy may still be landing in shared memory when the CTA exits.
     for (int s = 0; s < kStages; ++s)
@@ -570,6 +607,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     bool ok = true;
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       uint32_t idesc = S::kIdesc;
+      int chunk = 0;
+      if constexpr (Adapt::kOn) chunk = decode_tile(t, s_seg, s_pref, G, FT, S::kCH, p.tile_order).chunk;
       if (!kSwap && p.tail_m64) {
         const TileCoord c = decode_tile(t, s_seg, s_pref, G, FT, S::kCH, p.tile_order);
         if (c.nrows <= 64) idesc = S::kIdesc64;
@@ -577,7 +616,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + acc * S::kAccCols;
-      for (int kb = 0; kb < KB; ++kb) {
+      int blocks = KB;
+      for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
         tc_fence_after();
         const uint32_t a_addr = smem_u32(tiles + stage * S::kStageBytes);
@@ -593,6 +633,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         }
         tc_commit(&empty[stage]);
         if (++stage == kStages) { stage = 0; phase ^= 1; }
+        if constexpr (Adapt::kOn) {
+          if (kb == KB - 1) {  // the extension's length is known once the kernel before is done
+            pdl_wait();
+            blocks += __ldcg(&ad.count[chunk]) * ad.rblocks;
+          }
+        }
       }
       if (!ok) break;
       tc_commit(&tfull[acc]);
@@ -718,11 +764,12 @@ constexpr int gemm_pair_smem_bytes() {
   return kStages * PairShape<BN, kEpi>::kStageBytes + kStageOutBytes + 1024 + kSmemMisc;
 }
 
-template <int BN, int kEpi, int kStages>
+template <int BN, int kEpi, int kStages, class Adapt = NoAdapt>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     gemm_tc_pair_kernel(const __grid_constant__ CUtensorMap tmX,
                         const __grid_constant__ CUtensorMap tmW,
-                        const __grid_constant__ CUtensorMap tmO, const GemmParams p) {
+                        const __grid_constant__ CUtensorMap tmO, const GemmParams p,
+                        const __grid_constant__ Adapt ad) {
   using S = PairShape<BN, kEpi>;
   static_assert(kEpi != EPI_ROUTER, "the pair kernel has bf16 epilogues only");
   extern __shared__ uint8_t smem_raw[];
@@ -761,7 +808,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_desc(&tmX);
     tma_prefetch_desc(&tmW);
   }
-  pdl_wait();
+  if (!Adapt::kOn) pdl_wait();  // with adapters as in the 1-SM kernel
   pdl_launch_dependents();  // one CTA per SM, all resident: the next kernel may launch
 
   if (warp == 0) {  // group segments and tile prefix, as in the 1-SM kernel (256-row chunks)
@@ -828,6 +875,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         last_parity[stage] = phase;
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
+      if constexpr (Adapt::kOn) {
+        pdl_wait();
+        const int ext = ok ? __ldcg(&ad.count[c.chunk]) * ad.rblocks : 0;
+        for (int x = 0; x < ext; ++x) {
+          const int slot = x / ad.rblocks, rb = x - slot * ad.rblocks;
+          const int brow = __ldcg(&ad.list[static_cast<size_t>(c.chunk) * ad.cap + slot]) * p.Nw +
+                           c.ft * BN + static_cast<int>(rank) * (BN / 2);
+          if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+          uint8_t* sa = tiles + stage * S::kStageBytes;
+          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+          const uint32_t fb = cluster_addr(&full[stage], 0);
+          tma_load_2d_pair(&ad.v, fb, sa, x * 64, xrow);
+          tma_load_2d_pair(&ad.b, fb, sa + S::kABytes, rb * 64, brow);
+          issued[stage] = true;
+          last_parity[stage] = phase;
+          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        }
+      }
     }
     // The leader's full barriers count both CTAs' bytes: no copy is still landing afterwards.
     if (leader)
@@ -842,7 +907,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
-        for (int kb = 0; kb < KB; ++kb) {
+        int blocks = KB, chunk = 0;
+        if constexpr (Adapt::kOn) chunk = decode_tile(t, s_seg, s_pref, G, FT, S::kCH, p.tile_order).chunk;
+        for (int kb = 0; kb < blocks; ++kb) {
           if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
           tc_fence_after();
           const uint32_t a_addr = smem_u32(tiles + stage * S::kStageBytes);
@@ -853,6 +920,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                              S::kIdesc, (kb | k) != 0);
           tc_commit_pair(&empty[stage], 0x3);
           if (++stage == kStages) { stage = 0; phase ^= 1; }
+          if constexpr (Adapt::kOn) {
+            if (kb == KB - 1) {
+              pdl_wait();
+              blocks += __ldcg(&ad.count[chunk]) * ad.rblocks;
+            }
+          }
         }
         if (!ok) break;
         tc_commit_pair(&tfull[acc], 0x3);

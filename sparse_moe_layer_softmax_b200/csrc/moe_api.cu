@@ -9,6 +9,7 @@
 #include <mutex>
 #include <vector>
 
+#include "adapters.cuh"
 #include "common.cuh"
 #include "few_tokens.cuh"
 #include "gemm_splitk.cuh"
@@ -137,13 +138,35 @@ bool tail_m64_enabled() {
   return !(v && v[0] == '0');
 }
 
-template <bool kSwap, int BN, int kEpi, int kStages>
+// Operands of a projection's extension by adapters (GemmAdapt without its tensor maps): v [x_rows,
+// cap * rblocks * 64], the adapters' B matrices [n * Nout, rank].
+struct AdaptOperands {
+  const void* v;
+  const void* b;
+  const int* count;
+  const int* list;
+  int n, rank, cap, rblocks;
+};
+bool make_adapt(NoAdapt*, const AdaptOperands*, long, const GemmParams&, uint32_t, uint32_t) { return true; }
+bool make_adapt(GemmAdapt* g, const AdaptOperands* o, long x_rows, const GemmParams& p,
+                uint32_t x_box, uint32_t w_box) {
+  g->count = o->count;
+  g->list = o->list;
+  g->cap = o->cap;
+  g->rblocks = o->rblocks;
+  return make_tmap(&g->v, o->v, static_cast<uint64_t>(x_rows),
+                   static_cast<uint64_t>(o->cap) * o->rblocks * 64, x_box) &&
+         make_tmap(&g->b, o->b, static_cast<uint64_t>(o->n) * p.Nout, static_cast<uint64_t>(o->rank), w_box);
+}
+
+template <bool kSwap, int BN, int kEpi, int kStages, class Adapt = NoAdapt>
 moe_status_t launch_gemm(const void* X, long x_rows, const void* W, long w_rows,
-                         const GemmParams& p, long max_tiles, cudaStream_t st) {
+                         const GemmParams& p, long max_tiles, cudaStream_t st,
+                         const AdaptOperands* ops = nullptr) {
   using S = GemmShape<kSwap, BN, kEpi>;
   constexpr int smem = gemm_smem_bytes<kSwap, BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
-  auto kern = gemm_tc_kernel<kSwap, BN, kEpi, kStages>;
+  auto kern = gemm_tc_kernel<kSwap, BN, kEpi, kStages, Adapt>;
   static std::once_flag once;  // the attribute is per function; set it once per process
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
@@ -164,21 +187,24 @@ moe_status_t launch_gemm(const void* X, long x_rows, const void* W, long w_rows,
   CUtensorMap to = tx;
   q.out_tma = stages_output<kSwap, kEpi>() &&
               make_tmap(&to, p.out, static_cast<uint64_t>(x_rows), static_cast<uint64_t>(p.Nout), 32);
+  Adapt ad;
+  if (!make_adapt(&ad, ops, x_rows, p, S::kXBoxRows, S::kWBoxRows)) return MOE_ERR_CUDA;
   if (max_tiles <= 0) return MOE_OK;
   long grid = device_info().sms;
   if (grid <= 0) return MOE_ERR_CUDA;  // the SM count could not be read
   if (max_tiles < grid) grid = max_tiles;
-  launch_k(kern, static_cast<unsigned>(grid), kGemmThreads, smem, st, tx, tw, to, q);
+  launch_k(kern, static_cast<unsigned>(grid), kGemmThreads, smem, st, tx, tw, to, q, ad);
   return last_launch();
 }
 
 // CTA-pair variant: grid of whole clusters of 2.
-template <int BN, int kEpi, int kStages>
+template <int BN, int kEpi, int kStages, class Adapt = NoAdapt>
 moe_status_t launch_gemm_pair(const void* X, long x_rows, const void* W, long w_rows,
-                              const GemmParams& p, long max_tiles, cudaStream_t st) {
+                              const GemmParams& p, long max_tiles, cudaStream_t st,
+                              const AdaptOperands* ops = nullptr) {
   constexpr int smem = gemm_pair_smem_bytes<BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
-  auto kern = gemm_tc_pair_kernel<BN, kEpi, kStages>;
+  auto kern = gemm_tc_pair_kernel<BN, kEpi, kStages, Adapt>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
@@ -199,7 +225,9 @@ moe_status_t launch_gemm_pair(const void* X, long x_rows, const void* W, long w_
   long pairs = device_info().sms / 2;
   if (pairs <= 0) return MOE_ERR_CUDA;  // the SM count could not be read
   if (max_tiles < pairs) pairs = max_tiles;
-  launch_k(kern, static_cast<unsigned>(2 * pairs), kGemmThreads, smem, st, tx, tw, to, q);
+  Adapt ad;
+  if (!make_adapt(&ad, ops, x_rows, p, 128, BN / 2)) return MOE_ERR_CUDA;
+  launch_k(kern, static_cast<unsigned>(2 * pairs), kGemmThreads, smem, st, tx, tw, to, q, ad);
   return last_launch();
 }
 
@@ -494,16 +522,20 @@ int dense_k_splits(int rows, int nout, int K) {
 
 // Dense projection of at most kMaxSplitRows rows with its reduction split over clusters of
 // `splits` CTAs, which add their partial tiles in distributed shared memory.
-template <int kEpi>
+int split_smem(const NoAdapt&) { return gemm_splitk_smem_bytes(); }
+int split_smem(const SplitAdapt& ad) { return gemm_splitk_smem_bytes() + split_adapt_smem(ad.rank); }
+template <int kEpi, class Adapt = NoAdapt>
 moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long w_rows,
-                                const GemmParams& p, int splits, cudaStream_t st) {
-  constexpr int smem = gemm_splitk_smem_bytes();
-  static_assert(smem <= 232448, "shared memory budget");
-  auto kern = gemm_splitk_cluster_kernel<kEpi>;
+                                const GemmParams& p, int splits, cudaStream_t st,
+                                const Adapt& ad = Adapt{}) {
+  constexpr int most = gemm_splitk_smem_bytes() + (Adapt::kOn ? split_adapt_smem(MOE_ADAPTER_MAX_RANK) : 0);
+  static_assert(most <= 232448, "shared memory budget");
+  const int smem = split_smem(ad);
+  auto kern = gemm_splitk_cluster_kernel<kEpi, Adapt>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
   });
   if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
   if (x_rows > kSplitBN || splits < 2 || splits > kSplitMaxCluster || p.Nout % 128 ||
@@ -515,7 +547,7 @@ moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long 
   if (!make_tmap(&tw, W, static_cast<uint64_t>(w_rows), static_cast<uint64_t>(p.K), 128))
     return MOE_ERR_CUDA;
   launch_k_cluster(kern, static_cast<unsigned>(p.Nout / 128 * splits), kGemmThreads, smem, splits,
-                   st, tx, tw, p);
+                   st, tx, tw, p, ad);
   return last_launch();
 }
 
@@ -821,9 +853,7 @@ moe_status_t do_combine(const moe_config_t& c, const void* s, const int32_t* inv
   return last_launch();
 }
 
-moe_status_t do_latent_down(const moe_config_t& c, const void* u, const void* p_down, void* z,
-                            cudaStream_t st) {
-  if (c.T == 0) return MOE_OK;
+GemmParams latent_down_params(const moe_config_t& c, void* z) {
   GemmParams p{};
   p.G = 1;
   p.M = c.T;
@@ -832,6 +862,13 @@ moe_status_t do_latent_down(const moe_config_t& c, const void* u, const void* p_
   p.Nout = c.d_latent;
   p.out = z;
   dense_schedule(p, c.T);
+  return p;
+}
+
+moe_status_t do_latent_down(const moe_config_t& c, const void* u, const void* p_down, void* z,
+                            cudaStream_t st) {
+  if (c.T == 0) return MOE_OK;
+  const GemmParams p = latent_down_params(c, z);
   const int splits = dense_k_splits(c.T, c.d_latent, c.d_model);
   if (splits > 1) return launch_gemm_splitk<EPI_STORE>(u, c.T, p_down, c.d_latent, p, splits, st);
   Orient o;
@@ -841,9 +878,7 @@ moe_status_t do_latent_down(const moe_config_t& c, const void* u, const void* p_
   return run_gemm(EPI_STORE, o, bn, u, c.T, p_down, c.d_latent, p, st);
 }
 
-moe_status_t do_latent_up(const moe_config_t& c, const void* y, const void* p_up, const void* r,
-                          const float* g, void* out, cudaStream_t st) {
-  if (c.T == 0) return MOE_OK;
+GemmParams latent_up_params(const moe_config_t& c, const void* r, const float* g, void* out) {
   GemmParams p{};
   p.G = 1;
   p.M = c.T;
@@ -857,6 +892,13 @@ moe_status_t do_latent_up(const moe_config_t& c, const void* y, const void* p_up
   p.floor_ = c.resid_floor;
   p.resid_mode = c.resid_mode;
   dense_schedule(p, c.T);
+  return p;
+}
+
+moe_status_t do_latent_up(const moe_config_t& c, const void* y, const void* p_up, const void* r,
+                          const float* g, void* out, cudaStream_t st) {
+  if (c.T == 0) return MOE_OK;
+  const GemmParams p = latent_up_params(c, r, g, out);
   const int splits = dense_k_splits(c.T, c.d_model, c.d_latent);
   if (splits > 1) return launch_gemm_splitk<EPI_RESGATE>(y, c.T, p_up, c.d_model, p, splits, st);
   Orient o;
@@ -934,6 +976,11 @@ moe_status_t do_resid_update(const moe_config_t& c, const void* b, const void* r
 
 // ------------------------------------------------------------------ adapters
 
+// Ranges of the reduction of the tensor-core inner products over `chunks` row chunks.
+int adapter_splits(int chunks) {
+  return std::max(1, std::min(kAdMaxSplits, device_info().sms / std::max(chunks, 1)));
+}
+
 // Checks an adapter stack for the projections asked for (its pointers are looked at when T > 0).
 moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, const int32_t* which,
                             bool down, bool up) {
@@ -945,10 +992,104 @@ moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, con
   if (!ad->scale || !which) return MOE_ERR_INVALID_ARG;
   if (down && (!ad->down_a || !ad->down_b)) return MOE_ERR_INVALID_ARG;
   if (up && (!ad->up_a || !ad->up_b)) return MOE_ERR_INVALID_ARG;
-  if (!all_aligned({ad->scale, which, down ? ad->down_a : nullptr, down ? ad->down_b : nullptr,
+  // token_adapter is read one index at a time: a slice of a longer array may be passed
+  if (reinterpret_cast<uintptr_t>(which) & 3u) return MOE_ERR_ALIGNMENT;
+  if (!all_aligned({ad->scale, down ? ad->down_a : nullptr, down ? ad->down_b : nullptr,
                     up ? ad->up_a : nullptr, up ? ad->up_b : nullptr}))
     return MOE_ERR_ALIGNMENT;
   return MOE_OK;
+}
+
+// Workspace of the adapted projections, for either of the two (both widths).
+struct AdaptLayout {
+  size_t v, V, count, list, bad, total;
+};
+AdaptLayout adapt_layout(const moe_config_t& c, const moe_adapters_t& ad) {
+  AdaptLayout L{};
+  if (c.T == 0) return L;
+  const size_t T = c.T, n = ad.n_adapters, r = ad.rank, rb = (r + 63) / 64;
+  const int chunks = cdiv(c.T, kAdChunk);
+  const size_t splits = std::max(kAdSmallSplits, adapter_splits(chunks));
+  size_t o = 0;
+  auto take = [&](size_t bytes) { size_t at = o; o = align_up(o + bytes, 256); return at; };
+  L.v = take(splits * T * r * 4);
+  L.V = take(T * std::min<size_t>(n, std::min<size_t>(T, kAdMaxChunk)) * rb * 128);
+  L.count = take((T / 16 + 1) * 4);
+  L.list = take((T + kAdMaxChunk) * 4);
+  L.bad = take(n * 4);
+  L.total = o;
+  return L;
+}
+
+// y = x W^T plus every row's adapter, through the epilogue kEpi (p describes the projection).
+template <int kEpi>
+moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void* w, const GemmParams& p,
+                                const moe_adapters_t& ad, const void* a, const void* b,
+                                const int32_t* which, void* workspace, cudaStream_t st) {
+  const int T = c.T, K = p.K, n = ad.n_adapters, rank = ad.rank;
+  const AdaptLayout L = adapt_layout(c, ad);
+  float* v = at<float>(workspace, L.v);
+  const int dense_splits = dense_k_splits(T, p.Nout, K);
+  if (dense_splits > 1) {  // at most 64 rows
+    static_assert(kAdSmallRows == kMaxSplitRows && kAdSmallRows == kSplitBN, "rows of the small path");
+    launch_k(adapter_shrink_small_kernel, dim3(T, kAdSmallSplits, cdiv(rank, 16)), 128, 0, st,
+             static_cast<const uint16_t*>(x), T, K, static_cast<const uint16_t*>(a), ad.scale, which, n, rank, v);
+    moe_status_t s = last_launch();
+    if (s != MOE_OK) return s;
+    SplitAdapt sa{v, static_cast<const uint16_t*>(b), which, n, rank, kAdSmallSplits};
+    return launch_gemm_splitk<kEpi, SplitAdapt>(x, T, w, p.Nw, p, dense_splits, st, sa);
+  }
+  Orient o;
+  int bn;
+  pick_dense(T, p.Nout, &o, &bn);
+  if (bn == 0) return MOE_ERR_UNSUPPORTED;
+  const int CH = o == Orient::kSwap ? bn : o == Orient::kPair ? 256 : 128;  // rows of a tile
+  AdaptOperands ops{};
+  ops.v = at<void>(workspace, L.V);
+  ops.b = b;
+  ops.count = at<int>(workspace, L.count);
+  ops.list = at<int>(workspace, L.list);
+  ops.n = n;
+  ops.rank = rank;
+  ops.cap = std::min(n, std::min(CH, T));
+  ops.rblocks = cdiv(rank, 64);
+  const int chunks = cdiv(T, kAdChunk), splits = std::min(adapter_splits(chunks), K / 64);
+  {
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [&] {
+      attr_err = cudaFuncSetAttribute(adapter_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdSmem);
+    });
+    if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+    CUtensorMap tx, ta;
+    if (!make_tmap(&tx, x, static_cast<uint64_t>(T), static_cast<uint64_t>(K), kAdChunk) ||
+        !make_tmap(&ta, a, static_cast<uint64_t>(n) * rank, static_cast<uint64_t>(K), static_cast<uint32_t>(rank)))
+      return MOE_ERR_CUDA;
+    launch_k(adapter_shrink_kernel, dim3(chunks + n, splits), kGemmThreads, kAdSmem, st, tx, ta, T, K, which, n,
+             rank, chunks, static_cast<const uint16_t*>(b), static_cast<long>(p.Nout) * rank,
+             at<int>(workspace, L.bad), v);
+    launch_k(adapter_pack_kernel, cdiv(T, CH), kAdMaxChunk, 0, st, v, splits, T, which, n, rank, ad.scale,
+             at<int>(workspace, L.bad), CH, ops.cap, ops.rblocks, at<int>(workspace, L.count),
+             at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
+    moe_status_t s = last_launch(2);
+    if (s != MOE_OK) return s;
+  }
+  const int ft = o == Orient::kSwap ? p.Nout / 128 : cdiv(p.Nout, bn);
+  const long tiles = static_cast<long>(cdiv(T, CH)) * ft;
+#define AD(COND_, CALL_) if (COND_) return CALL_
+  if (o == Orient::kSwap) {
+    AD(bn == 16, (launch_gemm<true, 16, kEpi, 10, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 32, (launch_gemm<true, 32, kEpi, 9, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 64, (launch_gemm<true, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+  } else if (o == Orient::kPair) {
+    AD(bn == 256, (launch_gemm_pair<256, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+  } else {
+    AD(bn == 256, (launch_gemm<false, 256, kEpi, 4, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 128, (launch_gemm<false, 128, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 64, (launch_gemm<false, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+  }
+#undef AD
+  return MOE_ERR_UNSUPPORTED;
 }
 
 // ------------------------------------------------------------------ the layer for a few tokens
@@ -1384,12 +1525,34 @@ struct Taps {
   }
 };
 
+// Adapters of a whole-layer forward, with the workspace of the adapted projections.
+struct LayerAdapters {
+  const moe_adapters_t* ad = nullptr;  // nullptr: none
+  const int32_t* which = nullptr;
+  moe_status_t down(const moe_config_t& c, const void* u, const void* p_down, void* z, void* ws,
+                    cudaStream_t st) const {
+    if (!ad) return do_latent_down(c, u, p_down, z, st);
+    return adapted_projection<EPI_STORE>(c, u, p_down, latent_down_params(c, z), *ad, ad->down_a, ad->down_b,
+                                         which, ws, st);
+  }
+  moe_status_t up(const moe_config_t& c, const void* y, const void* p_up, const void* r, const float* g,
+                  void* out, void* ws, cudaStream_t st) const {
+    if (!ad) return do_latent_up(c, y, p_up, r, g, out, st);
+    return adapted_projection<EPI_RESGATE>(c, y, p_up, latent_up_params(c, r, g, out), *ad, ad->up_a, ad->up_b,
+                                           which, ws, st);
+  }
+};
+
 moe_status_t layer_forward_impl(const moe_config_t* cfg, const moe_weights_t* w, const void* u,
                                 const void* r, void* out, float* logits_out,
                                 int32_t* topk_idx_out, float* topk_w_out, const Taps& taps,
-                                void* workspace, size_t workspace_bytes, void* stream) {
+                                void* workspace, size_t workspace_bytes, void* stream,
+                                const LayerAdapters& la = LayerAdapters{}) {
+  size_t need = 0;
+  if (cfg && check_cfg(cfg) == MOE_OK)
+    need = layout(*cfg).total + (la.ad ? adapt_layout(*cfg, *la.ad).total : 0);
   moe_status_t s = check_forward(cfg, w, u, r, out, logits_out, topk_idx_out, topk_w_out,
-                                 workspace, workspace_bytes);
+                                 workspace, workspace_bytes, &need);
   if (s != MOE_OK) return s;
   const moe_config_t& c = *cfg;
   if (c.T == 0) return MOE_OK;
@@ -1403,6 +1566,7 @@ moe_status_t layer_forward_impl(const moe_config_t* cfg, const moe_weights_t* w,
   int32_t* inv = at<int32_t>(workspace, L.inv);
   void* x_perm = at<void>(workspace, L.x_perm);
   void* act = at<void>(workspace, L.act);
+  void* ad_ws = at<void>(workspace, L.total);
 
   prof_mark(st, 0);
   if (c.input_norm) {  // the branch input is the residual stream's norm (counted in stage 0)
@@ -1417,7 +1581,7 @@ moe_status_t layer_forward_impl(const moe_config_t* cfg, const moe_weights_t* w,
   const void* xin = u;
   if (latent) {
     void* z = at<void>(workspace, L.z_raw);
-    if ((s = do_latent_down(c, u, w->p_down, z, st)) != MOE_OK) return s;
+    if ((s = la.down(c, u, w->p_down, z, ad_ws, st)) != MOE_OK) return s;
     xin = z;
   }
   prof_mark(st, 2);
@@ -1444,13 +1608,13 @@ moe_status_t layer_forward_impl(const moe_config_t* cfg, const moe_weights_t* w,
   if (taps.t && (s = taps.copy(taps.t->y, y, static_cast<size_t>(c.T), c, st)) != MOE_OK) return s;
   prof_mark(st, 6);
   if (latent && !c.post_norm &&
-      (s = do_latent_up(c, y, w->p_up, r, w->resid_g, out, st)) != MOE_OK)
+      (s = la.up(c, y, w->p_up, r, w->resid_g, out, ad_ws, st)) != MOE_OK)
     return s;
   if (c.post_norm) {  // b to the workspace, then output norm + residual gate per row
     moe_config_t plain = c;
     plain.resid_mode = MOE_RESID_NONE;
     void* b = at<void>(workspace, L.b);
-    if ((s = do_latent_up(plain, y, w->p_up, nullptr, nullptr, b, st)) != MOE_OK) return s;
+    if ((s = la.up(plain, y, w->p_up, nullptr, nullptr, b, ad_ws, st)) != MOE_OK) return s;
     if ((s = do_resid_update(c, b, r, w->gamma_post, w->resid_g, out, st)) != MOE_OK) return s;
   }
   prof_mark(st, 7);
@@ -1481,6 +1645,61 @@ moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_weights_t
   tp.t = taps;
   return layer_forward_impl(cfg, w, u, r, out, logits_out, topk_idx_out, topk_w_out, tp,
                             workspace, workspace_bytes, stream);
+}
+
+moe_status_t moe_adapters_workspace_size(const moe_config_t* cfg, const moe_adapters_t* adapters,
+                                         size_t* bytes) {
+  moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  moe_config_t none = *cfg;
+  none.T = 0;
+  if ((s = check_adapters(none, adapters, nullptr, true, true)) != MOE_OK) return s;
+  if (!bytes) return MOE_ERR_INVALID_ARG;
+  *bytes = adapt_layout(*cfg, *adapters).total;
+  return MOE_OK;
+}
+
+moe_status_t moe_latent_down_adapters(const moe_config_t* cfg, const void* u, const void* p_down,
+                                      const moe_adapters_t* adapters, const int32_t* token_adapter,
+                                      void* z_raw, void* workspace, size_t workspace_bytes, void* stream) {
+  moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  if ((s = check_adapters(*cfg, adapters, token_adapter, true, false)) != MOE_OK) return s;
+  if (cfg->T == 0) return MOE_OK;
+  if (!u || !p_down || !z_raw) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({u, p_down, static_cast<const void*>(z_raw), workspace})) return MOE_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < adapt_layout(*cfg, *adapters).total) return MOE_ERR_WORKSPACE;
+  return LayerAdapters{adapters, token_adapter}.down(*cfg, u, p_down, z_raw, workspace,
+                                                     static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_latent_up_adapters(const moe_config_t* cfg, const void* y, const void* p_up,
+                                    const moe_adapters_t* adapters, const int32_t* token_adapter,
+                                    const void* r, const float* resid_g, void* out, void* workspace,
+                                    size_t workspace_bytes, void* stream) {
+  moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  if ((s = check_adapters(*cfg, adapters, token_adapter, false, true)) != MOE_OK) return s;
+  if (cfg->T == 0) return MOE_OK;
+  if (!y || !p_up || !out) return MOE_ERR_INVALID_ARG;
+  if (cfg->resid_mode != MOE_RESID_NONE && (!r || !resid_g)) return MOE_ERR_INVALID_ARG;
+  if (!all_aligned({y, p_up, r, static_cast<const void*>(resid_g), static_cast<const void*>(out), workspace}))
+    return MOE_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < adapt_layout(*cfg, *adapters).total) return MOE_ERR_WORKSPACE;
+  return LayerAdapters{adapters, token_adapter}.up(*cfg, y, p_up, r, resid_g, out, workspace,
+                                                   static_cast<cudaStream_t>(stream));
+}
+
+moe_status_t moe_layer_forward_adapters(const moe_config_t* cfg, const moe_weights_t* w,
+                                        const moe_adapters_t* adapters, const int32_t* token_adapter,
+                                        const void* u, const void* r, void* out, float* logits_out,
+                                        int32_t* topk_idx_out, float* topk_w_out, void* workspace,
+                                        size_t workspace_bytes, void* stream) {
+  moe_status_t s = check_cfg(cfg);
+  if (s != MOE_OK) return s;
+  if ((s = check_adapters(*cfg, adapters, token_adapter, true, true)) != MOE_OK) return s;
+  return layer_forward_impl(cfg, w, u, r, out, logits_out, topk_idx_out, topk_w_out, Taps{}, workspace,
+                            workspace_bytes, stream, LayerAdapters{adapters, token_adapter});
 }
 
 moe_status_t moe_few_workspace_size(const moe_config_t* cfg, const moe_adapters_t* adapters,

@@ -21,17 +21,20 @@
 
 #include "common.cuh"
 #include "few_tokens.cuh"
+#include "gemm_splitk.cuh"
 #include "gemm_tc.cuh"
 
 namespace moe {
 
 constexpr int kAdSmallRows = 64;     // rows of the small path
-constexpr int kAdSmallSplits = 8;    // ranges of the reduction, each a CTA of four warps
+constexpr int kAdSmallSplits = kSplitAdaptParts;  // ranges of the reduction, each a CTA
+constexpr int kAdSmallWarps = 8;
 constexpr int kAdChunk = 128;        // token rows of a tile of the tensor-core inner products
 constexpr int kAdGroupCols = 256;    // rows of A that one pass over the tokens multiplies
 constexpr int kAdStages = 4;
 constexpr int kAdMaxSplits = 16;
 constexpr int kAdMaxChunk = 256;     // rows of the projection's largest tile
+constexpr int kAdSlices = 8;         // parts of an adapter's B that are looked through apart
 constexpr int kAdStageBytes = kAdChunk * 128 + kAdGroupCols * 128;
 constexpr int kAdSmem = kAdStages * kAdStageBytes + 1024;
 
@@ -48,16 +51,16 @@ __device__ __forceinline__ int adapter_of(const int32_t* which, int t, int n, bo
 // v[split, t, :] = scale[a] * (A_a x_t over this split's columns).  CTA (t, split, rank tile) works if t
 // is the first token of its adapter, for all tokens of that adapter: A is read once.  Operands go from
 // global memory straight into m16n8k16 fragments (16 rows of A on M, 8 tokens on N; the reduction
-// index is permuted the same way in both, so every fragment is one 16-byte load); the four warps'
+// index is permuted the same way in both, so every fragment is one 16-byte load); the warps'
 // sums meet in shared memory.  Latency is all there is to this kernel: one token of rank 16 reads 262 KB.
-__global__ void __launch_bounds__(128)
+__global__ void __launch_bounds__(32 * kAdSmallWarps)
     adapter_shrink_small_kernel(const uint16_t* __restrict__ x, int T, int K,
                                 const uint16_t* __restrict__ A, const float* __restrict__ scale,
                                 const int32_t* __restrict__ which, int n, int rank,
                                 float* __restrict__ v) {
   __shared__ int s_list[kAdSmallRows];
   __shared__ int s_m[2];
-  __shared__ float s_red[4][16][kAdSmallRows + 1];
+  __shared__ float s_red[16][kAdSmallRows + 1];  // small, so that the projection's CTAs fit beside these
   pdl_wait();
   pdl_launch_dependents();
   const int t = blockIdx.x, split = blockIdx.y, r0 = blockIdx.z * 16;
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(128)
   const int m = s_m[0] + s_m[1];
 
   const int g = lane >> 2, q = lane & 3;
-  const int steps = K / 32, parts = kAdSmallSplits * 4, w = split * 4 + warp;
+  const int steps = K / 32, parts = kAdSmallSplits * kAdSmallWarps, w = split * kAdSmallWarps + warp;
   const int k_lo = static_cast<int>(static_cast<long>(w) * steps / parts);
   const int k_hi = static_cast<int>(static_cast<long>(w + 1) * steps / parts);
   const uint16_t* a0 = A + (static_cast<size_t>(a) * rank + min(r0 + g, rank - 1)) * K + q * 8;
@@ -94,22 +97,26 @@ __global__ void __launch_bounds__(128)
       }
     }
   }
+  for (int u = 0; u < kAdSmallWarps; ++u) {  // the warps' sums, in order
+    if (warp == u) {
 #pragma unroll
-  for (int j = 0; j < kAdSmallRows / 8; ++j) {
-    if (j * 8 < m) {
-      s_red[warp][g][j * 8 + 2 * q] = acc[j][0];
-      s_red[warp][g][j * 8 + 2 * q + 1] = acc[j][1];
-      s_red[warp][g + 8][j * 8 + 2 * q] = acc[j][2];
-      s_red[warp][g + 8][j * 8 + 2 * q + 1] = acc[j][3];
+      for (int j = 0; j < kAdSmallRows / 8; ++j) {
+        if (j * 8 < m) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            float* at = &s_red[g + (i >> 1) * 8][j * 8 + 2 * q + (i & 1)];
+            *at = u ? *at + acc[j][i] : acc[j][i];
+          }
+        }
+      }
     }
+    __syncthreads();
   }
-  __syncthreads();
   const float sc = scale[a];
-  for (int i = tid; i < 16 * m; i += 128) {
+  for (int i = tid; i < 16 * m; i += 32 * kAdSmallWarps) {
     const int row = i & 15, c = i >> 4;
     if (r0 + row < rank)
-      v[(static_cast<size_t>(split) * T + s_list[c]) * rank + r0 + row] =
-          sc * ((s_red[0][row][c] + s_red[1][row][c]) + (s_red[2][row][c] + s_red[3][row][c]));
+      v[(static_cast<size_t>(split) * T + s_list[c]) * rank + r0 + row] = sc * s_red[row][c];
   }
 }
 
@@ -124,7 +131,15 @@ __device__ __forceinline__ int adapter_slots(const int* s_ad, int rows, int* s_s
   int first = -1;  // first row with this row's adapter
   if (tid < rows && s_ad[tid] >= 0) {
     const int a = s_ad[tid];
-    for (first = 0; s_ad[first] != a; ++first) {}
+    int j = 0;
+    unsigned hit = 0;
+#pragma unroll 4
+    for (; j < rows; j += 4) {  // s_ad is padded with -1 to a multiple of four
+      const int4 v = *reinterpret_cast<const int4*>(s_ad + j);
+      hit = (v.x == a) | (v.y == a) << 1 | (v.z == a) << 2 | (v.w == a) << 3;
+      if (hit) break;
+    }
+    first = j + __ffs(static_cast<int>(hit)) - 1;
   }
   const unsigned lead = __ballot_sync(0xffffffffu, first == tid);
   if (lane == 0 && warp < 8) s_cnt[warp] = __popc(lead);
@@ -149,46 +164,58 @@ __device__ __forceinline__ int adapter_slots(const int* s_ad, int rows, int* s_s
   return total;
 }
 
+// Whether one of eight bf16 values is infinite or NaN (an exponent of all ones).
+__device__ __forceinline__ bool bf16x8_nonfinite(const uint4& q) {
+  const uint32_t w[4] = {q.x, q.y, q.z, q.w};
+  bool bad = false;
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    bad = bad || (w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u;
+  return bad;
+}
+
+// Looks through the used adapters' B matrices, kAdSlices CTAs to an adapter: byte [a, slice] of bad is 1
+// if the slice holds a non-finite value.  Runs beside the inner products (where few of their threads
+// are free, the same work took up to 100 us).
+__global__ void __launch_bounds__(256)
+    adapter_check_kernel(const int32_t* __restrict__ which, int T, const uint16_t* __restrict__ B, long b_elems,
+                         uint8_t* __restrict__ bad) {
+  pdl_wait();
+  pdl_launch_dependents();
+  const int tid = threadIdx.x, a = static_cast<int>(blockIdx.x) / kAdSlices;
+  const int slice = static_cast<int>(blockIdx.x) - a * kAdSlices;
+  bool used = false;
+#pragma unroll 8
+  for (int t = tid; t < T; t += 256) used = (which[t] == a) || used;
+  if (!__syncthreads_or(used)) return;
+  const long vecs = b_elems / 8, lo = vecs * slice / kAdSlices, hi = vecs * (slice + 1) / kAdSlices;
+  const uint4* p = reinterpret_cast<const uint4*>(B + static_cast<size_t>(a) * b_elems);
+  bool found = false;
+#pragma unroll 8
+  for (long j = lo + tid; j < hi; j += 256) {
+    const uint4 w = __ldg(p + j);
+    found = bf16x8_nonfinite(w) || found;
+  }
+  found = __syncthreads_or(found);
+  if (tid == 0) {
+    bad[a * kAdSlices + slice] = found;
+    if (found) latch_status(MOE_ERR_DEVICE_CHECK);
+  }
+}
+
 // v[split, t, :] = A_a x_t over this split's k-blocks, on the tensor cores: CTA (row chunk, split)
 // multiplies 128 token rows by the A rows of the adapters they use, up to 256 rows of A at a time,
-// and every token keeps its own adapter's columns.  Reading x sets the time (268 MB at prefill).  CTAs
-// past the chunks look through one adapter's B each: bad[a] = 1 if a used B holds a non-finite value.
+// and every token keeps its own adapter's columns.  Reading x sets the time (268 MB at prefill).
 __global__ void __launch_bounds__(kGemmThreads, 1)
     adapter_shrink_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmA,
-                          int T, int K, const int32_t* __restrict__ which, int n, int rank, int chunks,
-                          const uint16_t* __restrict__ B, long b_elems, int* __restrict__ bad,
+                          int T, int K, const int32_t* __restrict__ which, int n, int rank,
                           float* __restrict__ v) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kAdStages], empty[kAdStages], tfull[2], tempty[2];
   __shared__ uint32_t tmem_slot;
-  __shared__ int s_ad[kAdChunk], s_slot[kAdChunk], s_list[kAdChunk], s_cnt[9];
+  __shared__ __align__(16) int s_ad[kAdChunk];
+  __shared__ int s_slot[kAdChunk], s_list[kAdChunk], s_cnt[9];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-
-  if (static_cast<int>(blockIdx.x) >= chunks) {
-    pdl_wait();
-    pdl_launch_dependents();
-    if (blockIdx.y > 0) return;
-    const int a = static_cast<int>(blockIdx.x) - chunks;
-    bool used = false;
-    for (int t = tid; t < T; t += kGemmThreads) used = used || which[t] == a;
-    int found = 0;
-    if (__syncthreads_or(used)) {
-      const uint4* p = reinterpret_cast<const uint4*>(B + static_cast<size_t>(a) * b_elems);
-      for (long i = tid; i < b_elems / 8; i += kGemmThreads) {
-        const uint4 q = __ldg(p + i);
-        const uint32_t w[4] = {q.x, q.y, q.z, q.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j)  // an exponent of all ones
-          if ((w[j] & 0x7f80u) == 0x7f80u || (w[j] & 0x7f800000u) == 0x7f800000u) found = 1;
-      }
-    }
-    found = __syncthreads_or(found);
-    if (tid == 0) {
-      bad[a] = found;
-      if (found) latch_status(MOE_ERR_DEVICE_CHECK);
-    }
-    return;
-  }
 
   uint8_t* tiles = smem_raw + ((0u - smem_u32(smem_raw)) & 1023u);
   const int row0 = static_cast<int>(blockIdx.x) * kAdChunk, rows = min(kAdChunk, T - row0);
@@ -201,7 +228,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
   if (warp == 1) tmem_alloc(&tmem_slot, 512);
   if (tid == 0) { tma_prefetch_desc(&tmX); tma_prefetch_desc(&tmA); }
-  pdl_wait();
+  // The kernel before this one (adapter_check_kernel) started once x was complete, and runs beside it.
   pdl_launch_dependents();
   if (tid < kAdChunk) s_ad[tid] = tid < rows ? adapter_of(which, row0 + tid, n, blockIdx.y == 0) : -1;
   tc_fence_before();
@@ -284,6 +311,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       mbar_arrive(&tempty[acc]);
     }
   }
+  pdl_wait();  // the end of this kernel is the end of the one before, too
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -293,33 +321,42 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
-// The projection GEMM's operands of one row tile (CTA = tile of CH <= 256 rows): the adapters its rows
-// use (without the bad ones) and, per row, one block of rb * 64 columns for each of them: scale * v
-// (the splits added in order) in its own adapter's block, zeros in the others.
+// The projection GEMM's operands, tile by tile of CH <= 256 rows: the adapters the rows use (without
+// those whose B is broken) and, per row, one block of rb * 64 columns for each of them: scale * v (the
+// splits added in order) in its own adapter's block, zeros in the others.  Each CTA finds its tile's
+// adapters and writes `per` of its rows (one CTA a tile: 84 us for 333 rows in 3 tiles).
 __global__ void __launch_bounds__(kAdMaxChunk)
     adapter_pack_kernel(const float* __restrict__ v, int splits, int T, const int32_t* __restrict__ which,
-                        int n, int rank, const float* __restrict__ scale, const int* __restrict__ bad,
-                        int CH, int cap, int rb, int* __restrict__ count, int* __restrict__ list,
-                        uint16_t* __restrict__ V) {
-  __shared__ int s_ad[kAdMaxChunk], s_slot[kAdMaxChunk], s_list[kAdMaxChunk], s_cnt[9];
+                        int n, int rank, const float* __restrict__ scale,
+                        const unsigned long long* __restrict__ bad, int CH, int cap, int rb, int per,
+                        int* __restrict__ count, int* __restrict__ list, uint16_t* __restrict__ V) {
+  __shared__ __align__(16) int s_ad[kAdMaxChunk];
+  __shared__ int s_slot[kAdMaxChunk], s_list[kAdMaxChunk], s_cnt[9];
   // The projection may start: it multiplies x by W before it waits for this kernel.
   pdl_launch_dependents();
   pdl_wait();
-  const int tid = threadIdx.x, row0 = static_cast<int>(blockIdx.x) * CH, rows = min(CH, T - row0);
+  const int tid = threadIdx.x;
+  const int groups = (min(CH, T) + per - 1) / per;
+  const int tile = static_cast<int>(blockIdx.x) / groups, group = static_cast<int>(blockIdx.x) - tile * groups;
+  const int row0 = tile * CH, rows = min(CH, T - row0);
   int a = tid < rows ? adapter_of(which, row0 + tid, n, false) : -1;
-  if (a >= 0 && bad[a]) a = -1;
+  if (a >= 0 && bad[a] != 0ull) a = -1;  // its eight slices
   s_ad[tid] = a;
   __syncthreads();
   const int ns = adapter_slots(s_ad, rows, s_slot, s_list, s_cnt);
-  if (tid == 0) count[blockIdx.x] = ns;
-  for (int i = tid; i < ns; i += kAdMaxChunk) list[static_cast<size_t>(blockIdx.x) * cap + i] = s_list[i];
+  if (group == 0) {
+    if (tid == 0) count[tile] = ns;
+    if (tid < ns) list[tile * adapt_list_pitch(cap) + tid] = s_list[tid];
+  }
+  const int first = group * per, mine = min(per, rows - first);
   const int vec = ns * rb * 8;  // 16-byte units of a row
   const size_t pitch = static_cast<size_t>(cap) * rb * 64;
-  for (int i = tid; i < rows * vec; i += kAdMaxChunk) {
-    const int row = i / vec, u = i - row * vec, c = u % (rb * 8) * 8;
+  for (int i = tid; i < mine * vec; i += kAdMaxChunk) {
+    const int r = i / vec, row = first + r, u = i - r * vec, c = u % (rb * 8) * 8;
     uint4 o = make_uint4(0, 0, 0, 0);
     if (u / (rb * 8) == s_slot[row] && c < rank) {
       float f[8] = {};
+#pragma unroll 8
       for (int s = 0; s < splits; ++s) {
         const float4* p = reinterpret_cast<const float4*>(v + (static_cast<size_t>(s) * T + row0 + row) * rank + c);
         const float4 x = __ldcg(p), y = __ldcg(p + 1);

@@ -86,6 +86,29 @@ struct GemmAdapt {
   const int* list;
   int cap, rblocks;
 };
+// The k-block at which a tile's extension is looked up, so that the answer is there when it is needed.
+__device__ __forceinline__ int adapt_early(int KB) { return KB > 12 ? KB - 12 : 0; }
+// A tile's list starts on a 16-byte boundary: the producer takes four adapters a load.
+__host__ __device__ constexpr size_t adapt_list_pitch(int cap) { return (static_cast<size_t>(cap) + 3) / 4 * 4; }
+// The extension's adapters in order, read one load ahead of their use (an L2 load per adapter in its turn
+// cost 16 adapters a tile some 25 us).
+struct AdaptList {
+  const int4* at = nullptr;
+  int4 cur, nxt;
+  int slots = 0;
+  __device__ void open(const GemmAdapt& ad, int chunk) {
+    at = reinterpret_cast<const int4*>(ad.list + chunk * adapt_list_pitch(ad.cap));
+    nxt = __ldcg(at);
+    slots = __ldcg(&ad.count[chunk]);
+  }
+  __device__ int operator()(int slot) {
+    if ((slot & 3) == 0) {
+      cur = nxt;
+      if (slot + 4 < slots) nxt = __ldcg(at + slot / 4 + 1);
+    }
+    return (slot & 3) == 0 ? cur.x : (slot & 3) == 1 ? cur.y : (slot & 3) == 2 ? cur.z : cur.w;
+  }
+};
 
 // Shared memory that stages the bf16 output of the normal-orientation epilogues: one 4 KB
 // buffer (32 rows x 128 bytes) per epilogue warp.
@@ -546,7 +569,14 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     for (int t = blockIdx.x; t < total && ok; t += gridDim.x) {
       TileCoord c = decode_tile(t, s_seg, s_pref, G, FT, S::kCH, p.tile_order);
       const int wrow = c.g * p.Nw + c.ft * S::kFO;
+      AdaptList adapters;
       for (int kb = 0; kb < KB; ++kb) {
+        if constexpr (Adapt::kOn) {
+          if (kb == adapt_early(KB)) {
+            pdl_wait();
+            adapters.open(ad, c.chunk);
+          }
+        }
         // weight-stream-bound layers (l2_hints): L2 fetches the weight k-block one ring ahead, so
         // more DRAM requests are in flight than the shared-memory ring holds
         if (!kSwap && p.l2_hints && kb + kStages < KB) {
@@ -581,20 +611,19 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
       if constexpr (Adapt::kOn) {
-        pdl_wait();
-        const int ext = ok ? __ldcg(&ad.count[c.chunk]) * ad.rblocks : 0;
-        for (int x = 0; x < ext; ++x) {
-          const int slot = x / ad.rblocks, rb = x - slot * ad.rblocks;
-          const int brow = __ldcg(&ad.list[static_cast<size_t>(c.chunk) * ad.cap + slot]) * p.Nw + c.ft * S::kFO;
-          if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
-          uint8_t* sa = tiles + stage * S::kStageBytes;
-          uint8_t* sb = sa + S::kABytes;
-          mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
-          tma_load_2d(&ad.v, &full[stage], kSwap ? sb : sa, x * 64, c.row0);
-          tma_load_2d(&ad.b, &full[stage], kSwap ? sa : sb, rb * 64, brow);
-          issued[stage] = true;
-          last_parity[stage] = phase;
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        for (int slot = 0; slot < adapters.slots && ok; ++slot) {
+          const int brow = adapters(slot) * p.Nw + c.ft * S::kFO;
+          for (int rb = 0; rb < ad.rblocks; ++rb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+            uint8_t* sa = tiles + stage * S::kStageBytes;
+            uint8_t* sb = sa + S::kABytes;
+            mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
+            tma_load_2d(&ad.v, &full[stage], kSwap ? sb : sa, (slot * ad.rblocks + rb) * 64, c.row0);
+            tma_load_2d(&ad.b, &full[stage], kSwap ? sa : sb, rb * 64, brow);
+            issued[stage] = true;
+            last_parity[stage] = phase;
+            if (++stage == kStages) { stage = 0; phase ^= 1; }
+          }
         }
       }
     }
@@ -616,7 +645,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       if (!mbar_wait(&tempty[acc], acc_phase ^ 1)) break;
       tc_fence_after();
       const uint32_t d = tmem_base + acc * S::kAccCols;
-      int blocks = KB;
+      int blocks = KB, ext = 0;
+      const int early = adapt_early(KB);
       for (int kb = 0; kb < blocks; ++kb) {
         if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
         tc_fence_after();
@@ -634,10 +664,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         tc_commit(&empty[stage]);
         if (++stage == kStages) { stage = 0; phase ^= 1; }
         if constexpr (Adapt::kOn) {
-          if (kb == KB - 1) {  // the extension's length is known once the kernel before is done
+          if (kb == early) {  // the extension's length, known once the kernel before is done
             pdl_wait();
-            blocks += __ldcg(&ad.count[chunk]) * ad.rblocks;
+            ext = __ldcg(&ad.count[chunk]) * ad.rblocks;
           }
+          if (kb == KB - 1) blocks += ext;
         }
       }
       if (!ok) break;
@@ -862,7 +893,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int xrow = c.row0 + 128 * static_cast<int>(rank);
       const int wrow = S::kDual ? c.g * p.Nw + (leader ? 0 : p.Nw / 2) + c.ft * (BN / 2)
                                 : c.g * p.Nw + c.ft * BN + static_cast<int>(rank) * (BN / 2);
+      AdaptList adapters;
       for (int kb = 0; kb < KB; ++kb) {
+        if constexpr (Adapt::kOn) {
+          if (kb == adapt_early(KB)) {
+            pdl_wait();
+            adapters.open(ad, c.chunk);
+          }
+        }
         if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
         uint8_t* sa = tiles + stage * S::kStageBytes;
         uint8_t* sb = sa + S::kABytes;
@@ -876,21 +914,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
       if constexpr (Adapt::kOn) {
-        pdl_wait();
-        const int ext = ok ? __ldcg(&ad.count[c.chunk]) * ad.rblocks : 0;
-        for (int x = 0; x < ext; ++x) {
-          const int slot = x / ad.rblocks, rb = x - slot * ad.rblocks;
-          const int brow = __ldcg(&ad.list[static_cast<size_t>(c.chunk) * ad.cap + slot]) * p.Nw +
-                           c.ft * BN + static_cast<int>(rank) * (BN / 2);
-          if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
-          uint8_t* sa = tiles + stage * S::kStageBytes;
-          if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
-          const uint32_t fb = cluster_addr(&full[stage], 0);
-          tma_load_2d_pair(&ad.v, fb, sa, x * 64, xrow);
-          tma_load_2d_pair(&ad.b, fb, sa + S::kABytes, rb * 64, brow);
-          issued[stage] = true;
-          last_parity[stage] = phase;
-          if (++stage == kStages) { stage = 0; phase ^= 1; }
+        for (int slot = 0; slot < adapters.slots && ok; ++slot) {
+          const int brow = adapters(slot) * p.Nw + c.ft * BN + static_cast<int>(rank) * (BN / 2);
+          for (int rb = 0; rb < ad.rblocks; ++rb) {
+            if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
+            uint8_t* sa = tiles + stage * S::kStageBytes;
+            if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
+            const uint32_t fb = cluster_addr(&full[stage], 0);
+            tma_load_2d_pair(&ad.v, fb, sa, (slot * ad.rblocks + rb) * 64, xrow);
+            tma_load_2d_pair(&ad.b, fb, sa + S::kABytes, rb * 64, brow);
+            issued[stage] = true;
+            last_parity[stage] = phase;
+            if (++stage == kStages) { stage = 0; phase ^= 1; }
+          }
         }
       }
     }
@@ -907,7 +943,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (!mbar_wait(&tempty[acc], acc_phase ^ 1)) break;
         tc_fence_after();
         const uint32_t d = tmem_base + acc * BN;
-        int blocks = KB, chunk = 0;
+        int blocks = KB, chunk = 0, ext = 0;
+        const int early = adapt_early(KB);
         if constexpr (Adapt::kOn) chunk = decode_tile(t, s_seg, s_pref, G, FT, S::kCH, p.tile_order).chunk;
         for (int kb = 0; kb < blocks; ++kb) {
           if (!mbar_wait(&full[stage], phase)) { ok = false; break; }
@@ -921,10 +958,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           tc_commit_pair(&empty[stage], 0x3);
           if (++stage == kStages) { stage = 0; phase ^= 1; }
           if constexpr (Adapt::kOn) {
-            if (kb == KB - 1) {
+            if (kb == early) {
               pdl_wait();
-              blocks += __ldcg(&ad.count[chunk]) * ad.rblocks;
+              ext = __ldcg(&ad.count[chunk]) * ad.rblocks;
             }
+            if (kb == KB - 1) blocks += ext;
           }
         }
         if (!ok) break;

@@ -522,13 +522,13 @@ int dense_k_splits(int rows, int nout, int K) {
 
 // Dense projection of at most kMaxSplitRows rows with its reduction split over clusters of
 // `splits` CTAs, which add their partial tiles in distributed shared memory.
-int split_smem(const NoAdapt&) { return gemm_splitk_smem_bytes(); }
-int split_smem(const SplitAdapt& ad) { return gemm_splitk_smem_bytes() + split_adapt_smem(ad.rank); }
+int split_smem(const NoAdapt&) { return gemm_splitk_smem_bytes<NoAdapt>(); }
+int split_smem(const SplitAdapt& ad) { return gemm_splitk_smem_bytes<SplitAdapt>() + split_adapt_smem(ad.rank); }
 template <int kEpi, class Adapt = NoAdapt>
 moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long w_rows,
                                 const GemmParams& p, int splits, cudaStream_t st,
                                 const Adapt& ad = Adapt{}) {
-  constexpr int most = gemm_splitk_smem_bytes() + (Adapt::kOn ? split_adapt_smem(MOE_ADAPTER_MAX_RANK) : 0);
+  constexpr int most = gemm_splitk_smem_bytes<Adapt>() + (Adapt::kOn ? split_adapt_smem(MOE_ADAPTER_MAX_RANK) : 0);
   static_assert(most <= 232448, "shared memory budget");
   const int smem = split_smem(ad);
   auto kern = gemm_splitk_cluster_kernel<kEpi, Adapt>;
@@ -546,7 +546,7 @@ moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long 
     return MOE_ERR_CUDA;
   if (!make_tmap(&tw, W, static_cast<uint64_t>(w_rows), static_cast<uint64_t>(p.K), 128))
     return MOE_ERR_CUDA;
-  launch_k_cluster(kern, static_cast<unsigned>(p.Nout / 128 * splits), kGemmThreads, smem, splits,
+  launch_k_cluster(kern, static_cast<unsigned>(p.Nout / 128 * splits), split_threads<Adapt>(), smem, splits,
                    st, tx, tw, p, ad);
   return last_launch();
 }
@@ -1015,8 +1015,10 @@ AdaptLayout adapt_layout(const moe_config_t& c, const moe_adapters_t& ad) {
   L.v = take(splits * T * r * 4);
   L.V = take(T * std::min<size_t>(n, std::min<size_t>(T, kAdMaxChunk)) * rb * 128);
   L.count = take((T / 16 + 1) * 4);
-  L.list = take((T + kAdMaxChunk) * 4);
-  L.bad = take(n * 4);
+  // a tile of CH >= 16 rows lists up to CH adapters, rounded up to 4
+  L.list = take((T + kAdMaxChunk + T / 4 + 4) * 4);
+  static_assert(kAdSlices == 8, "one 64-bit word an adapter");
+  L.bad = take(n * 8);
   L.total = o;
   return L;
 }
@@ -1032,11 +1034,11 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
   const int dense_splits = dense_k_splits(T, p.Nout, K);
   if (dense_splits > 1) {  // at most 64 rows
     static_assert(kAdSmallRows == kMaxSplitRows && kAdSmallRows == kSplitBN, "rows of the small path");
-    launch_k(adapter_shrink_small_kernel, dim3(T, kAdSmallSplits, cdiv(rank, 16)), 128, 0, st,
+    launch_k(adapter_shrink_small_kernel, dim3(T, kAdSmallSplits, cdiv(rank, 16)), 32 * kAdSmallWarps, 0, st,
              static_cast<const uint16_t*>(x), T, K, static_cast<const uint16_t*>(a), ad.scale, which, n, rank, v);
     moe_status_t s = last_launch();
     if (s != MOE_OK) return s;
-    SplitAdapt sa{v, static_cast<const uint16_t*>(b), which, n, rank, kAdSmallSplits};
+    SplitAdapt sa{v, static_cast<const uint16_t*>(b), which, n, rank};
     return launch_gemm_splitk<kEpi, SplitAdapt>(x, T, w, p.Nw, p, dense_splits, st, sa);
   }
   Orient o;
@@ -1065,13 +1067,17 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
     if (!make_tmap(&tx, x, static_cast<uint64_t>(T), static_cast<uint64_t>(K), kAdChunk) ||
         !make_tmap(&ta, a, static_cast<uint64_t>(n) * rank, static_cast<uint64_t>(K), static_cast<uint32_t>(rank)))
       return MOE_ERR_CUDA;
-    launch_k(adapter_shrink_kernel, dim3(chunks + n, splits), kGemmThreads, kAdSmem, st, tx, ta, T, K, which, n,
-             rank, chunks, static_cast<const uint16_t*>(b), static_cast<long>(p.Nout) * rank,
-             at<int>(workspace, L.bad), v);
-    launch_k(adapter_pack_kernel, cdiv(T, CH), kAdMaxChunk, 0, st, v, splits, T, which, n, rank, ad.scale,
-             at<int>(workspace, L.bad), CH, ops.cap, ops.rblocks, at<int>(workspace, L.count),
-             at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
-    moe_status_t s = last_launch(2);
+    launch_k(adapter_check_kernel, n * kAdSlices, 256, 0, st, which, T, static_cast<const uint16_t*>(b),
+             static_cast<long>(p.Nout) * rank, at<uint8_t>(workspace, L.bad));
+    launch_k(adapter_shrink_kernel, dim3(chunks, splits), kGemmThreads, kAdSmem, st, tx, ta, T, K, which, n,
+             rank, v);
+    // rows a CTA writes: few, so that small batches use many CTAs; more at prefill, where finding the tile's
+    // adapters is what a CTA spends its time on
+    const int per = T >= 4096 ? 32 : 8;
+    launch_k(adapter_pack_kernel, cdiv(T, CH) * cdiv(std::min(T, CH), per), kAdMaxChunk, 0, st, v, splits, T, which, n, rank, ad.scale,
+             at<unsigned long long>(workspace, L.bad), CH, ops.cap, ops.rblocks, per,
+             at<int>(workspace, L.count), at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
+    moe_status_t s = last_launch(3);
     if (s != MOE_OK) return s;
   }
   const int ft = o == Orient::kSwap ? p.Nout / 128 : cdiv(p.Nout, bn);

@@ -53,7 +53,7 @@ __device__ __forceinline__ int adapter_of(const int32_t* which, int t, int n, bo
 // global memory straight into m16n8k16 fragments (16 rows of A on M, 8 tokens on N; the reduction
 // index is permuted the same way in both, so every fragment is one 16-byte load); the warps'
 // sums meet in shared memory.  Latency is all there is to this kernel: one token of rank 16 reads 262 KB.
-__global__ void __launch_bounds__(32 * kAdSmallWarps)
+__global__ void __launch_bounds__(32 * kAdSmallWarps, 3)
     adapter_shrink_small_kernel(const uint16_t* __restrict__ x, int T, int K,
                                 const uint16_t* __restrict__ A, const float* __restrict__ scale,
                                 const int32_t* __restrict__ which, int n, int rank,

@@ -37,8 +37,10 @@ namespace moe {
 
 constexpr int kFewTokens = 8;                  // tokens on the MMA's N side
 constexpr int kFewSlots = kFewTokens * kMaxTopK;
-constexpr int kFewMmaWarps = 8;                // warps that multiply
-constexpr int kFewEpiWarps = 4;                // warps that finish tiles
+// Warps that multiply.  With the three that finish tiles and the producer they are twelve, three on each of
+// the SM's schedulers with 168 registers a thread (with thirteen and 128, the tile loop spilled).
+constexpr int kFewMmaWarps = 8;
+constexpr int kFewEpiWarps = 3;                // warps that finish tiles
 constexpr int kFewMma = 32 * kFewMmaWarps, kFewEpi = 32 * kFewEpiWarps;
 constexpr int kFewWork = kFewMma + kFewEpi;    // threads of both groups
 constexpr int kFewThreads = kFewWork + 32;     // and the producer warp
@@ -123,7 +125,7 @@ struct FewTables {
   int expert[kFewSlots];               // ascending
   int count[kFewSlots];                // slots routed to that expert (at most T)
   uint8_t slot[kFewSlots][kFewTokens]; // those slots, in token order
-  int own[kFewMmaWarps], most[kFewMmaWarps];
+  int own[kMaxExperts / 32], most[kMaxExperts / 32];  // per group of 32 experts
   // adapters: the distinct ones the tokens use, and each token's (-1: none)
   int ndist_ad;
   int ad[kFewTokens];
@@ -174,12 +176,14 @@ struct FewTiles {
   // This CTA's tiles.  Expert stages: a contiguous run (at most a few experts per CTA) of the first
   // 13/16 of the tiles; the others are taken one by one from a shared counter, since SMs stream at
   // rates some 10% apart (static shares alone: the slowest CTA of one token's first expert stage ended 7 us
-  // after the mean).  With fewer than 8 tiles a CTA the counter's latency would cost more than it
-  // evens out.  Dense stages: strided, so that their leading tiles start at once on as many CTAs.
+  // after the mean).  With fewer than 8 tiles a CTA, or tiles of less than 64 KB, the counter's latency and
+  // the rows of another expert would cost more than it evens out.  Dense stages: strided, so that their
+  // leading tiles start at once on as many CTAs.
   __device__ int fixed(int phase) const {
     const int N = total(phase);
     if (phase != FEW_UP1 && phase != FEW_DOWN2) return N;
-    return N >= 8 * static_cast<int>(gridDim.x) ? static_cast<int>(N * 13l / 16) : N;
+    const int tile_bytes = (phase == FEW_UP1 ? p.E : p.H) * kFewRows * (kF32 ? 4 : 2);
+    return N >= 8 * static_cast<int>(gridDim.x) && tile_bytes >= 65536 ? static_cast<int>(N * 13l / 16) : N;
   }
   __device__ void range(int phase, int& i, int& end, int& step) const {
     const int N = fixed(phase);
@@ -498,47 +502,64 @@ __device__ __forceinline__ void few_topk(const FewParams& p, FewTables& tb, int 
 __device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, volatile int* abort_,
                                           uint64_t* routed, int warp, int lane) {
   few_wait<FEW_MMA>(p.bar, 0, abort_);
-  if (warp < p.T) few_topk(p, tb, warp, lane);
+  for (int t = warp; t < p.T; t += kFewMmaWarps) few_topk(p, tb, t, lane);
   few_bar<FEW_MMA>();
-  // distinct experts in ascending order, each with its slots in token order (thread = expert)
+  // distinct experts in ascending order, each with its slots in token order: warp w looks at the
+  // groups w, w + 8, ... of 32 experts, a lane at one expert
+  constexpr int kGroups = kMaxExperts / 32;
   const int slots = p.T * p.k, tid = warp * 32 + lane;
-  unsigned long long hits = 0;  // slots routed to this thread's expert
-#pragma unroll 1
-  for (int s = 0; s < slots; s += 4) {
-    const int4 v = *reinterpret_cast<const int4*>(&tb.idx[s]);  // entries past the last slot: masked
-    const unsigned f = (v.x == tid) | (v.y == tid) << 1 | (v.z == tid) << 2 | (v.w == tid) << 3;
-    hits |= static_cast<unsigned long long>(f) << s;
-  }
-  if (slots < 64) hits &= (1ull << slots) - 1ull;
-  const int cnt = min(__popcll(hits), kFewTokens);
-  const unsigned has = __ballot_sync(0xffffffffu, cnt > 0);
-  const unsigned most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(cnt));
-  if (lane == 0) {
-    tb.own[warp] = __popc(has);
-    tb.most[warp] = static_cast<int>(most);
+  unsigned long long hits[(kGroups + kFewMmaWarps - 1) / kFewMmaWarps];
+  unsigned has[(kGroups + kFewMmaWarps - 1) / kFewMmaWarps];
+#pragma unroll
+  for (int i = 0; i * kFewMmaWarps < kGroups; ++i) {
+    const int g = warp + i * kFewMmaWarps, e = g * 32 + lane;
+    hits[i] = 0ull;  // slots routed to expert e
+    for (int s = 0; s < slots; s += 4) {
+      const int4 v = *reinterpret_cast<const int4*>(&tb.idx[s]);  // entries past the last slot: masked
+      const unsigned f = (v.x == e) | (v.y == e) << 1 | (v.z == e) << 2 | (v.w == e) << 3;
+      hits[i] |= static_cast<unsigned long long>(f) << s;
+    }
+    if (slots < 64) hits[i] &= (1ull << slots) - 1ull;
+    if (g >= kGroups) hits[i] = 0ull;
+    has[i] = __ballot_sync(0xffffffffu, hits[i] != 0ull);
+    const unsigned most = __reduce_max_sync(0xffffffffu, static_cast<unsigned>(__popcll(hits[i])));
+    if (lane == 0 && g < kGroups) {
+      tb.own[g] = __popc(has[i]);
+      tb.most[g] = static_cast<int>(most);
+    }
   }
   few_bar<FEW_MMA>();
-  int at = __popc(has & ((1u << lane) - 1u)), total = 0, rows = 0;
+  int before[kGroups + 1], rows = 0;
+  before[0] = 0;
 #pragma unroll
-  for (int w = 0; w < kFewMmaWarps; ++w) {
-    at += w < warp ? tb.own[w] : 0;
-    total += tb.own[w];
-    rows = max(rows, tb.most[w]);
+  for (int g = 0; g < kGroups; ++g) {
+    before[g + 1] = before[g] + tb.own[g];
+    rows = max(rows, tb.most[g]);
   }
-  if (cnt > 0) {
-    tb.expert[at] = tid;
-    tb.count[at] = cnt;
-    for (int q = 0; q < cnt; ++q) {
-      tb.slot[at][q] = static_cast<uint8_t>(__ffsll(hits) - 1);
-      hits &= hits - 1ull;
+#pragma unroll
+  for (int i = 0; i * kFewMmaWarps < kGroups; ++i) {
+    const int g = warp + i * kFewMmaWarps;
+    int at = __popc(has[i] & ((1u << lane) - 1u));
+#pragma unroll
+    for (int q = 0; q < kGroups; ++q)
+      if (q == g) at += before[q];
+    if (hits[i] != 0ull) {
+      const int cnt = min(__popcll(hits[i]), kFewTokens);
+      tb.expert[at] = g * 32 + lane;
+      tb.count[at] = cnt;
+      for (int q = 0; q < cnt; ++q) {
+        tb.slot[at][q] = static_cast<uint8_t>(__ffsll(hits[i]) - 1);
+        hits[i] &= hits[i] - 1ull;
+      }
     }
   }
   if (tid == 0) {
-    tb.dist = total;
-    tb.rows = p.resident ? p.T : rows;
-    if (!p.L) tb.rows = p.T;  // the first expert stage reads u where the router left it
-    tb.stages = p.ring_stages[tb.rows];
-    tb.turns = p.ring_turns[tb.rows];
+    tb.dist = before[kGroups];
+    // rows the expert stages hold; without latent projections they read u where the router left it
+    const int held = p.resident || !p.L ? p.T : min(rows, p.T);
+    tb.rows = held;
+    tb.stages = p.ring_stages[held];
+    tb.turns = p.ring_turns[held];
   }
   if (blockIdx.x == 0 && tid < slots) {
     if (p.idx_out) p.idx_out[tid] = tb.idx[tid];
@@ -570,6 +591,105 @@ struct FewRing {
   }
 };
 
+// `rows` rows of K fp32 values from global memory into the activation region, by `threads` threads of
+// which this is number `id`.  Row r comes from source row slots[r] / div, or r without slots.  Four loads
+// a thread are in flight: one by one, each took its 0.5 us or more (eight tokens' y: 9 us).
+template <bool kF32>
+__device__ __forceinline__ void few_load_rows(FewAct act, int id, int threads, int rows, int K, const float* src,
+                                           const uint8_t* slots, int div, const float* gain) {
+  const int vec = K / 4;
+  for (int row = 0; row < rows; ++row) {
+    const int from_row = slots ? slots[row] / div : row;
+    const float4* from = reinterpret_cast<const float4*>(src + static_cast<size_t>(from_row) * K);
+    for (int i = id; i < vec; i += 4 * threads) {
+      float4 v[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        if (i + u * threads < vec) v[u] = __ldcg(from + i + u * threads);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int c = i + u * threads;
+        if (c >= vec) break;
+        if (gain) {
+          const float4 g = *reinterpret_cast<const float4*>(gain + c * 4);
+          v[u].x *= 1.0f + g.x; v[u].y *= 1.0f + g.y; v[u].z *= 1.0f + g.z; v[u].w *= 1.0f + g.w;
+        }
+        few_act_put4<kF32>(act, row, c * 4, v[u]);
+      }
+    }
+  }
+}
+
+// u of every token, or C_in(r) rounded to bf16, into the activation region, by all working threads.
+template <bool kF32>
+__device__ __forceinline__ void few_load_u(const FewParams& p, FewAct act, int tid) {
+  const void* src = p.input_norm ? p.r : p.u;
+  const int vec = p.d * (kF32 ? 4 : 2) / 16;
+  for (int t = 0; t < p.T; ++t) {
+    const uint4* row = static_cast<const uint4*>(src) + static_cast<size_t>(t) * vec;
+    char* dst = act.base + t * act.pitch;
+#pragma unroll 4
+    for (int i = tid; i < vec; i += kFewWork) *reinterpret_cast<uint4*>(dst + i * 16) = row[i];
+  }
+  few_bar<FEW_WORK>();
+  if constexpr (!kF32) {
+    if (p.input_norm) {
+      const int warp = tid >> 5, lane = tid & 31;
+      if (warp < p.T) {  // one warp per token
+        uint16_t* row = reinterpret_cast<uint16_t*>(act.base + warp * act.pitch);
+        float ss = 0.0f;
+        for (int i = lane; i < p.d; i += 32) { const float x = bf16_to_f32(row[i]); ss = fmaf(x, x, ss); }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float inv = 1.0f / sqrtf(ss / p.d + p.eps_block);
+        for (int i = lane; i < p.d; i += 32)
+          row[i] = f32_to_bf16((1.0f + p.gamma_in[i]) * (bf16_to_f32(row[i]) * inv));
+      }
+      few_bar<FEW_WORK>();
+    }
+  }
+}
+
+// I_gamma and the weighted sum of this CTA's share of the columns: y, or without latent projections the
+// layer's output.  By all working threads.
+template <bool kF32>
+__device__ __forceinline__ void few_combine(const FewParams& p, FewTables& tb, int tid) {
+  const int warp = tid >> 5, lane = tid & 31, k = p.k;
+  const int cols = kFewMma, blocks = (p.E + cols - 1) / cols;
+  for (int unit = blockIdx.x; unit < p.T * blocks; unit += gridDim.x) {
+    const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
+    const bool mine = warp < kFewMmaWarps && c < p.E;
+    float s[kMaxTopK];  // in flight while the norms are summed
+#pragma unroll
+    for (int j = 0; j < kMaxTopK; ++j)
+      s[j] = mine && j < k ? __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) : 0.0f;
+    if (warp < k) {
+      float inv = 1.0f;
+      if (p.expert_norm) {
+        const float* part = p.ss + static_cast<size_t>(t * k + warp) * (p.E / 16);
+        float q = 0.0f;
+#pragma unroll 4
+        for (int j = lane; j < p.E / 16; j += 32) q += __ldcg(&part[j]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
+        inv = 1.0f / sqrtf(q / p.E + p.eps);
+      }
+      if (lane == 0) tb.inv[warp] = inv;
+    }
+    few_bar<FEW_WORK>();
+    if (mine) {
+      float y = 0.0f;
+#pragma unroll
+      for (int j = 0; j < kMaxTopK; ++j)
+        if (j < k) y = fmaf(tb.w[t * k + j], s[j] * tb.inv[j], y);
+      if (p.L) p.y[static_cast<size_t>(t) * p.E + c] = y;
+      else if (kF32) static_cast<float*>(p.out)[static_cast<size_t>(t) * p.E + c] = y;
+      else static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.E + c] = f32_to_bf16(y);
+    }
+    few_bar<FEW_WORK>();
+  }
+}
+
 // Zeroes the grid-barrier and tile counters of one call.
 __global__ void few_init_kernel(unsigned* bar) {
   pdl_wait();
@@ -581,12 +701,12 @@ __global__ void few_init_kernel(unsigned* bar) {
 // the CTA's stream (one ring stage) belongs to warp c % W (W <= 8), so W stages are in work at once and
 // a tile's chunks meet as up to W partial tiles in shared memory.  The ring holds a multiple
 // of W stages: then one warp alone waits on a stage's barrier, phase after phase (with another number
-// a warp could come to a stage whose previous fill has not landed, and take its parity for its own).  Warps 8-11 add the partial tiles
+// a warp could come to a stage whose previous fill has not landed, and take its parity for its own).  Warps 8-10 add the partial tiles
 // in chunk order and finish the tile (one barrier per tile among all warps had kept the stream at half
-// its rate).  Warp 12 is the producer.
+// its rate).  Warp 11 is the producer.
 template <bool kF32>
 __global__ void __launch_bounds__(kFewThreads, 1)
-    few_layer_kernel(const FewParams p, const __grid_constant__ FewMaps maps) {
+    few_layer_kernel(const __grid_constant__ FewParams p, const __grid_constant__ FewMaps maps) {
   extern __shared__ uint8_t few_smem[];
   char* ring = reinterpret_cast<char*>(few_smem) + ((0u - smem_u32(few_smem)) & 1023u);
   char* act_mem = ring + p.stages * kFewStageBytes;  // dense stages; the expert stages' lies higher
@@ -699,7 +819,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
   const bool mma = warp < kFewMmaWarps;
   const int et = tid - kFewMma;            // thread of the finishing group
-  const int er = et & 15, ec = et >> 4;    // its tile row and column
+  const int er = et & 15, ec = et >> 4;    // its tile row and first column, of kEpiCols at a time
+  constexpr int kEpiCols = kFewEpi / kFewRows;
   FewRing rg(p.stages, p.turns);
   unsigned tile_no = 0, qn = 0;
   FewAct act;
@@ -743,48 +864,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     for (int o = 8; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
     return q;
   };
-  // Rows of fp32 values from global memory into the activation region, by the multiplying warps.
-  auto load_rows = [&](int rows, int K, const float* src, auto row_of, const float* gain) {
-    const int vec = K / 4;
-    for (int i = tid; i < rows * vec; i += kFewMma) {
-      const int row = i / vec, c = (i - row * vec) * 4;
-      float4 v = __ldcg(reinterpret_cast<const float4*>(src + static_cast<size_t>(row_of(row)) * K + c));
-      if (gain) {
-        const float4 g = *reinterpret_cast<const float4*>(gain + c);
-        v.x *= 1.0f + g.x; v.y *= 1.0f + g.y; v.z *= 1.0f + g.z; v.w *= 1.0f + g.w;
-      }
-      few_act_put4<kF32>(act, row, c, v);
-    }
-    few_bar<FEW_MMA>();
-  };
-
   for (int ph = FEW_IN; ph <= FEW_OUT; ++ph) {
     // ------------------------------------------------------------ what the stage multiplies
     if (ph == FEW_IN) {  // u, or C_in(r)
       act = few_act<kF32>(act_mem, T, p.d, false);
-      const void* src = p.input_norm ? p.r : p.u;
-      const int vec = p.d * (kF32 ? 4 : 2) / 16;
-      for (int t = 0; t < T; ++t) {
-        const uint4* row = static_cast<const uint4*>(src) + static_cast<size_t>(t) * vec;
-        char* dst = act.base + t * act.pitch;
-        for (int i = tid; i < vec; i += kFewWork) *reinterpret_cast<uint4*>(dst + i * 16) = row[i];
-      }
-      few_bar<FEW_WORK>();
-      if constexpr (!kF32) {
-        if (p.input_norm) {
-          if (warp < T) {  // one warp per token
-            uint16_t* row = reinterpret_cast<uint16_t*>(act.base + warp * act.pitch);
-            float ss = 0.0f;
-            for (int i = lane; i < p.d; i += 32) { const float x = bf16_to_f32(row[i]); ss = fmaf(x, x, ss); }
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            const float inv = 1.0f / sqrtf(ss / p.d + p.eps_block);
-            for (int i = lane; i < p.d; i += 32)
-              row[i] = f32_to_bf16((1.0f + p.gamma_in[i]) * (bf16_to_f32(row[i]) * inv));
-          }
-          few_bar<FEW_WORK>();
-        }
-      }
+      few_load_u<kF32>(p, act, tid);
     } else if (ph == FEW_UP1) {
       // The routing tables, by the multiplying warps; then (1 + gamma_pre) z.  C_pre's 1/rms is one
       // factor per token, applied when a tile is finished.  Without latent projections the products
@@ -796,7 +880,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (p.L) act = few_act<kF32>(act_mem, tb.rows, p.E, true);
       if (mma) {
         if (p.L && p.resident)
-          load_rows(T, p.E, p.z, [](int c) { return c; }, p.pre_norm ? p.gamma_pre : nullptr);
+          few_load_rows<kF32>(act, tid, kFewMma, T, p.E, p.z, nullptr, 1, p.pre_norm ? p.gamma_pre : nullptr);
+        few_bar<FEW_MMA>();
       } else if (p.pre_norm) {
         for (int t = warp - kFewMmaWarps; t < T; t += kFewEpiWarps) {
           float q = 0.0f;
@@ -811,48 +896,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       act = few_act<kF32>(act_mem, tb.rows, p.H, true);
       if (mma) few_wait<FEW_MMA>(p.bar, 2, abort_);
     } else {
-      // I_gamma and the weighted sum: y, or without latent projections the layer's output
       few_wait<FEW_WORK>(p.bar, 3, abort_);
-      const int cols = kFewMma, blocks = (p.E + cols - 1) / cols;
-      for (int unit = blockIdx.x; unit < T * blocks; unit += gridDim.x) {
-        const int t = unit / blocks, c = (unit - t * blocks) * cols + tid;
-        float s[kMaxTopK];  // in flight while the norms are summed
-#pragma unroll
-        for (int j = 0; j < kMaxTopK; ++j)
-          s[j] = mma && c < p.E && j < k ? __ldcg(&p.s[static_cast<size_t>(t * k + j) * p.E + c]) : 0.0f;
-        if (warp < k) {
-          float inv = 1.0f;
-          if (p.expert_norm) {
-            const float* part = p.ss + static_cast<size_t>(t * k + warp) * (p.E / 16);
-            float q = 0.0f;
-            for (int j = lane; j < p.E / 16; j += 32) q += __ldcg(&part[j]);
-#pragma unroll
-            for (int o = 16; o > 0; o >>= 1) q += __shfl_xor_sync(0xffffffffu, q, o);
-            inv = 1.0f / sqrtf(q / p.E + p.eps);
-          }
-          if (lane == 0) tb.inv[warp] = inv;
-        }
-        few_bar<FEW_WORK>();
-        if (mma && c < p.E) {
-          float y = 0.0f;
-#pragma unroll
-          for (int j = 0; j < kMaxTopK; ++j)
-            if (j < k) y = fmaf(tb.w[t * k + j], s[j] * tb.inv[j], y);
-          if (p.L) p.y[static_cast<size_t>(t) * p.E + c] = y;
-          else if (kF32) static_cast<float*>(p.out)[static_cast<size_t>(t) * p.E + c] = y;
-          else static_cast<uint16_t*>(p.out)[static_cast<size_t>(t) * p.E + c] = f32_to_bf16(y);
-        }
-        few_bar<FEW_WORK>();
-      }
+      few_combine<kF32>(p, tb, tid);
       if (!p.L) return;
       few_arrive<FEW_WORK>(p.bar, 4);
       few_wait<FEW_WORK>(p.bar, 4, abort_);
       rg.resize(p.stages, p.turns);
       act_mem = ring + p.stages * kFewStageBytes;
       act = few_act<kF32>(act_mem, T, p.L, true);
-      for (int t = 0; t < T; ++t)
-        for (int c = tid * 4; c < p.L; c += 4 * kFewWork)
-          few_act_put4<kF32>(act, t, c, __ldcg(reinterpret_cast<const float4*>(p.y + static_cast<size_t>(t) * p.L + c)));
+      few_load_rows<kF32>(act, tid, kFewWork, T, p.L, p.y, nullptr, 1, nullptr);
       few_bar<FEW_WORK>();
     }
 
@@ -889,10 +941,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const bool per_expert = ph == FEW_DOWN2 || (ph == FEW_UP1 && p.L && !p.resident);
         if (per_expert && t.e != loaded) {  // its rows, once every warp is past the previous ones
           few_bar<FEW_MMA>();
-          if (ph == FEW_UP1)
-            load_rows(m, p.E, p.z, [&](int c) { return tb.slot[t.e][c] / k; }, p.pre_norm ? p.gamma_pre : nullptr);
-          else
-            load_rows(m, p.H, p.a, [&](int c) { return static_cast<int>(tb.slot[t.e][c]); }, nullptr);
+          const bool up1 = ph == FEW_UP1;
+          few_load_rows<kF32>(act, tid, kFewMma, m, up1 ? p.E : p.H, up1 ? p.z : p.a, tb.slot[t.e], up1 ? k : 1,
+                              up1 && p.pre_norm ? p.gamma_pre : nullptr);
+          few_bar<FEW_MMA>();
           loaded = t.e;
         }
         const int W = static_cast<int>(rg.W), turn0 = static_cast<int>((rg.c - rg.c0) % rg.W);
@@ -962,12 +1014,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         have_v = true;
       }
       const bool dual = t.kind == FEW_GATEUP && p.swiglu;
-      // SwiGLU tiles: 16 columns of 8 features, of which the upper columns are empty
-      const int row = dual ? et & 7 : er, col = dual ? et >> 3 : ec;
+      // SwiGLU tiles: up to 12 columns of 8 features; others: 6 columns of 16 rows at a time
+      const int row = dual ? et & 7 : er;
       const int f = t.r0 + row;
       const float gain = t.kind == FEW_EXPERT_OUT && p.expert_norm ? 1.0f + p.gamma_expert[f] : 1.0f;
-      // the tile's value at (row, col), and at (row + 8, col)
       if (!*abort_ && !mbar_wait(&red_full[rb], rturn)) *abort_ = 1;
+#pragma unroll 1
+      for (int col = dual ? et >> 3 : ec, left = dual ? 1 : m; left > 0; left -= kEpiCols, col += kEpiCols) {
+      // the tile's value at (row, col), and at (row + 8, col)
       float v = 0.0f, up = 0.0f;
       {
         const float* at = red + rb * kFewRedFloats + row * kFewRedPitch + min(col, kFewTokens - 1);
@@ -981,8 +1035,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
           }
         }
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&red_empty[rb]);
+      if (left <= kEpiCols) {  // the last read
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&red_empty[rb]);
+      }
       const bool mine = col < m;
       switch (t.kind) {
         case FEW_ROUTER:
@@ -1037,6 +1093,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             const float q = column_sum(v * v);
             if (row == 0 && mine) p.bss[static_cast<size_t>(col) * (p.d / 16) + t.r0 / 16] = q;
           }
+      }
       }
     }
     if (!mma) {

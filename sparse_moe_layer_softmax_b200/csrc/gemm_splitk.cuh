@@ -53,7 +53,7 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
 // Low-rank adapters of the batch's rows: row t adds B_a v_t, a = which[t], v_t the sum of the partial
 // inner products v[s, t, :] (already scaled) that the kernel just before this one writes.
 constexpr int kSplitAdaptParts = 4;
-constexpr int kSplitAdaptThreads = 384;  // that make the terms: the 128 epilogue threads and 256 more
+constexpr int kSplitAdaptThreads = 256;  // that make the terms: the 128 epilogue threads and 128 more
 __device__ __forceinline__ void split_adapt_bar() {
   asm volatile("bar.sync 2, %0;" ::"n"(kSplitAdaptThreads) : "memory");
 }
@@ -85,8 +85,8 @@ constexpr int split_adapt_smem(int rank) {
 // The adapter terms B_a v_t of this CTA's 128/NS features for every row, into s_term[row][feature].  Runs
 // in kSplitAdaptThreads threads while the tile's weights stream in, and behind that stream every load
 // takes about 3 us: what counts is how few of them wait for one another.  So the rows are grouped by
-// adapter, the B rows of as many adapters as the buffer holds come in as one bulk copy each (a part of B
-// is contiguous), and v's partial sums as one batch of loads; then m16n8k16 products put 16 features on M,
+// adapter, the adapters' B rows come in as one bulk copy each (a part of B is contiguous), as many as
+// half a buffer holds while the other half is in use, and v's partial sums as one batch of loads; then m16n8k16 products put 16 features on M,
 // eight of an adapter's rows on N and the rank on K.  (Loading B into fragments adapter by adapter, 64
 // adapters of rank 16 took 60 us; a thread to 8 features on the CUDA cores, 12 of rank 64 also 60.)
 // v enters as hi + lo, so the term keeps fp32's accuracy to 2^-17.
@@ -102,7 +102,7 @@ __device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmPar
   SplitRows& r = *reinterpret_cast<SplitRows*>(s_term + kSplitBN * kSplitTermPitch);
   char* s_b = reinterpret_cast<char*>(&r + 1);
   const int f0 = ft * 128 + static_cast<int>(rank) * kFs;
-  const int b_bytes = kFs * ad.rank * 2, fit = kSplitBBytes / b_bytes;  // at least 2 adapters at a time
+  const int b_bytes = kFs * ad.rank * 2, fit = kSplitBBytes / 2 / b_bytes;  // adapters in half of the buffer
 
   if (et < kSplitBN) {
     int a = -1;
@@ -149,20 +149,23 @@ __device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmPar
     r.first[gid] = begin;
     r.start[et] = begin;
   }
-  if (et == 0) {
-    r.first[groups] = rows;
-    if (groups) mbar_arrive_expect_tx(b_full, static_cast<uint32_t>(min(fit, groups)) * b_bytes);
-  }
+  if (et == 0) r.first[groups] = rows;
   split_adapt_bar();
   if (mine >= 0)
     r.row[r.start[__ffsll(static_cast<long long>(same)) - 1] + __popcll(same & ((1ull << et) - 1ull))] = et;
-  // copies of the B rows of adapters [g0, g0 + fit), a thread to an adapter
-  auto fetch = [&](int g0) {
-    for (int i = et; i < min(fit, groups - g0); i += kSplitAdaptThreads)
-      bulk_load(s_b + i * b_bytes, ad.b + (static_cast<size_t>(r.adapter[g0 + i]) * p.Nout + f0) * ad.rank,
-                static_cast<uint32_t>(b_bytes), b_full);
+  // Copies of the B rows of round k's adapters [k fit, k fit + fit) into half k & 1 of the buffer, a thread
+  // to an adapter.  (A copy may land before its bytes are expected: the phase ends with the one arrival.)
+  auto fetch = [&](int k) {
+    const int m = min(fit, groups - k * fit);
+    if (m <= 0) return;
+    if (et == 0) mbar_arrive_expect_tx(&b_full[k & 1], static_cast<uint32_t>(m) * b_bytes);
+    for (int i = et; i < m; i += kSplitAdaptThreads)
+      bulk_load(s_b + (k & 1) * (kSplitBBytes / 2) + i * b_bytes,
+                ad.b + (static_cast<size_t>(r.adapter[k * fit + i]) * p.Nout + f0) * ad.rank,
+                static_cast<uint32_t>(b_bytes), &b_full[k & 1]);
   };
   fetch(0);
+  fetch(1);
   pdl_wait();  // v
   // Four columns of a row at a time, two of them and all their parts in flight; the padding of the rank
   // to whole 32s is zero.
@@ -213,13 +216,13 @@ __device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmPar
   const uint32_t v0 = smem_u32(s_v) + q * 16, b0 = smem_u32(s_b) + g * ad.rank * 2 + q * 16;
   bool ok = true;
   for (int g0 = 0, round = 0; g0 < groups; g0 += fit, ++round) {
-    ok = ok && mbar_wait(b_full, round & 1);
+    ok = ok && mbar_wait(&b_full[round & 1], round >> 1 & 1);
     const int pairs = min(fit, groups - g0) * (kFs / 16);
     // (adapter, 16-feature tile), a warp at a time
     for (int w = warp; w < pairs; w += kSplitAdaptThreads / 32) {
       const int gi = w / (kFs / 16), mt = w % (kFs / 16), gr = g0 + gi;
       const int r0 = r.first[gr], r1 = r.first[gr + 1];
-      const uint32_t b = b0 + gi * b_bytes + mt * 32 * ad.rank;
+      const uint32_t b = b0 + (round & 1) * (kSplitBBytes / 2) + gi * b_bytes + mt * 32 * ad.rank;
       for (int c0 = r0; c0 < r1; c0 += 8) {  // eight rows on N
         const bool has = c0 + g < r1;
         const uint32_t v = v0 + (has ? r.row[c0 + g] : 0) * pitch;
@@ -251,10 +254,9 @@ __device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmPar
         }
       }
     }
-    if (g0 + fit < groups) {
-      split_adapt_bar();  // every warp is done with the buffer
-      if (et == 0) mbar_arrive_expect_tx(b_full, static_cast<uint32_t>(min(fit, groups - g0 - fit)) * b_bytes);
-      fetch(g0 + fit);
+    if (g0 + 2 * fit < groups) {
+      split_adapt_bar();  // every warp is done with this half
+      fetch(round + 2);
     }
   }
 }
@@ -345,7 +347,8 @@ __device__ __forceinline__ void splitk_reduce(const GemmParams& p, const float* 
 template <class Adapt>
 constexpr int split_threads() { return Adapt::kOn ? 64 + kSplitAdaptThreads : kGemmThreads; }
 template <int kEpi, class Adapt = NoAdapt>
-__global__ void __launch_bounds__(split_threads<Adapt>(), 1)
+// (With adapters two CTAs' worth of registers at most: room for the inner products' CTAs beside this one.)
+__global__ void __launch_bounds__(split_threads<Adapt>(), Adapt::kOn ? 2 : 1)
     gemm_splitk_cluster_kernel(const __grid_constant__ CUtensorMap tmX,
                                const __grid_constant__ CUtensorMap tmW, const GemmParams p,
                                const Adapt ad) {
@@ -359,8 +362,8 @@ __global__ void __launch_bounds__(split_threads<Adapt>(), 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(tiles + kStages * S::kStageBytes);
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;
-  uint64_t* b_full = tfull + 1;  // adapters: their B rows have landed
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 1);
+  uint64_t* b_full = tfull + 1;  // adapters: the B rows in either half of their buffer have landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(b_full + 2);
 
   char* s_adapt = reinterpret_cast<char*>(tiles) + kStages * S::kStageBytes + 256;  // adapters only
 
@@ -375,7 +378,8 @@ __global__ void __launch_bounds__(split_threads<Adapt>(), 1)
   if (threadIdx.x == 32) {
     for (int s = 0; s < kStages; ++s) { mbar_init(&full[s], 1); mbar_init(&empty[s], 1); }
     mbar_init(tfull, 1);
-    mbar_init(b_full, 1);
+    mbar_init(&b_full[0], 1);
+    mbar_init(&b_full[1], 1);
     fence_barrier_init();
   }
   if (warp == 1) tmem_alloc(tmem_slot, kSplitBN);

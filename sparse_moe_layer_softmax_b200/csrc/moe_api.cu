@@ -140,6 +140,9 @@ bool tail_m64_enabled() {
 
 // Operands of a projection's extension by adapters (GemmAdapt without its tensor maps): v [x_rows,
 // cap * rblocks * 64], the adapters' B matrices [n * Nout, rank].
+struct Nothing {
+  void operator()() const {}
+};
 struct AdaptOperands {
   const void* v;
   const void* b;
@@ -159,10 +162,10 @@ bool make_adapt(GemmAdapt* g, const AdaptOperands* o, long x_rows, const GemmPar
          make_tmap(&g->b, o->b, static_cast<uint64_t>(o->n) * p.Nout, static_cast<uint64_t>(o->rank), w_box);
 }
 
-template <bool kSwap, int BN, int kEpi, int kStages, class Adapt = NoAdapt>
+template <bool kSwap, int BN, int kEpi, int kStages, class Adapt = NoAdapt, class Before = Nothing>
 moe_status_t launch_gemm(const void* X, long x_rows, const void* W, long w_rows,
                          const GemmParams& p, long max_tiles, cudaStream_t st,
-                         const AdaptOperands* ops = nullptr) {
+                         const AdaptOperands* ops = nullptr, const Before& before = Before{}) {
   using S = GemmShape<kSwap, BN, kEpi>;
   constexpr int smem = gemm_smem_bytes<kSwap, BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
@@ -193,15 +196,16 @@ moe_status_t launch_gemm(const void* X, long x_rows, const void* W, long w_rows,
   long grid = device_info().sms;
   if (grid <= 0) return MOE_ERR_CUDA;  // the SM count could not be read
   if (max_tiles < grid) grid = max_tiles;
+  before();
   launch_k(kern, static_cast<unsigned>(grid), kGemmThreads, smem, st, tx, tw, to, q, ad);
   return last_launch();
 }
 
 // CTA-pair variant: grid of whole clusters of 2.
-template <int BN, int kEpi, int kStages, class Adapt = NoAdapt>
+template <int BN, int kEpi, int kStages, class Adapt = NoAdapt, class Before = Nothing>
 moe_status_t launch_gemm_pair(const void* X, long x_rows, const void* W, long w_rows,
                               const GemmParams& p, long max_tiles, cudaStream_t st,
-                              const AdaptOperands* ops = nullptr) {
+                              const AdaptOperands* ops = nullptr, const Before& before = Before{}) {
   constexpr int smem = gemm_pair_smem_bytes<BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
   auto kern = gemm_tc_pair_kernel<BN, kEpi, kStages, Adapt>;
@@ -227,6 +231,7 @@ moe_status_t launch_gemm_pair(const void* X, long x_rows, const void* W, long w_
   if (max_tiles < pairs) pairs = max_tiles;
   Adapt ad;
   if (!make_adapt(&ad, ops, x_rows, p, 128, BN / 2)) return MOE_ERR_CUDA;
+  before();
   launch_k(kern, static_cast<unsigned>(2 * pairs), kGemmThreads, smem, st, tx, tw, to, q, ad);
   return last_launch();
 }
@@ -524,10 +529,10 @@ int dense_k_splits(int rows, int nout, int K) {
 // `splits` CTAs, which add their partial tiles in distributed shared memory.
 int split_smem(const NoAdapt&) { return gemm_splitk_smem_bytes<NoAdapt>(); }
 int split_smem(const SplitAdapt& ad) { return gemm_splitk_smem_bytes<SplitAdapt>() + split_adapt_smem(ad.rank); }
-template <int kEpi, class Adapt = NoAdapt>
+template <int kEpi, class Adapt = NoAdapt, class Before = Nothing>
 moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long w_rows,
                                 const GemmParams& p, int splits, cudaStream_t st,
-                                const Adapt& ad = Adapt{}) {
+                                const Adapt& ad = Adapt{}, const Before& before = Before{}) {
   constexpr int most = gemm_splitk_smem_bytes<Adapt>() + (Adapt::kOn ? split_adapt_smem(MOE_ADAPTER_MAX_RANK) : 0);
   static_assert(most <= 232448, "shared memory budget");
   const int smem = split_smem(ad);
@@ -546,6 +551,7 @@ moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long 
     return MOE_ERR_CUDA;
   if (!make_tmap(&tw, W, static_cast<uint64_t>(w_rows), static_cast<uint64_t>(p.K), 128))
     return MOE_ERR_CUDA;
+  before();
   launch_k_cluster(kern, static_cast<unsigned>(p.Nout / 128 * splits), split_threads<Adapt>(), smem, splits,
                    st, tx, tw, p, ad);
   return last_launch();
@@ -1034,12 +1040,14 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
   const int dense_splits = dense_k_splits(T, p.Nout, K);
   if (dense_splits > 1) {  // at most 64 rows
     static_assert(kAdSmallRows == kMaxSplitRows && kAdSmallRows == kSplitBN, "rows of the small path");
-    launch_k(adapter_shrink_small_kernel, dim3(T, kAdSmallSplits, cdiv(rank, 16)), 32 * kAdSmallWarps, 0, st,
-             static_cast<const uint16_t*>(x), T, K, static_cast<const uint16_t*>(a), ad.scale, which, n, rank, v);
-    moe_status_t s = last_launch();
-    if (s != MOE_OK) return s;
     SplitAdapt sa{v, static_cast<const uint16_t*>(b), which, n, rank};
-    return launch_gemm_splitk<kEpi, SplitAdapt>(x, T, w, p.Nw, p, dense_splits, st, sa);
+    // launched right before the projection, with nothing for the host to do in between
+    return launch_gemm_splitk<kEpi, SplitAdapt>(x, T, w, p.Nw, p, dense_splits, st, sa, [&] {
+      launch_k(adapter_shrink_small_kernel, dim3(T, kAdSmallSplits, cdiv(rank, 16)), 32 * kAdSmallWarps, 0, st,
+               static_cast<const uint16_t*>(x), T, K, static_cast<const uint16_t*>(a), ad.scale, which, n, rank,
+               v);
+      last_launch();
+    });
   }
   Orient o;
   int bn;
@@ -1056,43 +1064,43 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
   ops.cap = std::min(n, std::min(CH, T));
   ops.rblocks = cdiv(rank, 64);
   const int chunks = cdiv(T, kAdChunk), splits = std::min(adapter_splits(chunks), K / 64);
-  {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-      attr_err = cudaFuncSetAttribute(adapter_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdSmem);
-    });
-    if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
-    CUtensorMap tx, ta;
-    if (!make_tmap(&tx, x, static_cast<uint64_t>(T), static_cast<uint64_t>(K), kAdChunk) ||
-        !make_tmap(&ta, a, static_cast<uint64_t>(n) * rank, static_cast<uint64_t>(K), static_cast<uint32_t>(rank)))
-      return MOE_ERR_CUDA;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [&] {
+    attr_err = cudaFuncSetAttribute(adapter_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdSmem);
+  });
+  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  CUtensorMap tx, ta;
+  if (!make_tmap(&tx, x, static_cast<uint64_t>(T), static_cast<uint64_t>(K), kAdChunk) ||
+      !make_tmap(&ta, a, static_cast<uint64_t>(n) * rank, static_cast<uint64_t>(K), static_cast<uint32_t>(rank)))
+    return MOE_ERR_CUDA;
+  auto before = [&] {
+    unsigned long long* bad = at<unsigned long long>(workspace, L.bad);
     launch_k(adapter_check_kernel, n * kAdSlices, 256, 0, st, which, T, static_cast<const uint16_t*>(b),
-             static_cast<long>(p.Nout) * rank, at<uint8_t>(workspace, L.bad));
+             static_cast<long>(p.Nout) * rank, reinterpret_cast<uint8_t*>(bad));
     launch_k(adapter_shrink_kernel, dim3(chunks, splits), kGemmThreads, kAdSmem, st, tx, ta, T, K, which, n,
              rank, v);
     // rows a CTA writes: few, so that small batches use many CTAs; more at prefill, where finding the tile's
     // adapters is what a CTA spends its time on
     const int per = T >= 4096 ? 32 : 8;
-    launch_k(adapter_pack_kernel, cdiv(T, CH) * cdiv(std::min(T, CH), per), kAdMaxChunk, 0, st, v, splits, T, which, n, rank, ad.scale,
-             at<unsigned long long>(workspace, L.bad), CH, ops.cap, ops.rblocks, per,
-             at<int>(workspace, L.count), at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
-    moe_status_t s = last_launch(3);
-    if (s != MOE_OK) return s;
-  }
+    launch_k(adapter_pack_kernel, cdiv(T, CH) * cdiv(std::min(T, CH), per), kAdMaxChunk, 0, st, v, splits, T,
+             which, n, rank, ad.scale, bad, CH, ops.cap, ops.rblocks, per, at<int>(workspace, L.count),
+             at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
+    last_launch(3);
+  };
   const int ft = o == Orient::kSwap ? p.Nout / 128 : cdiv(p.Nout, bn);
   const long tiles = static_cast<long>(cdiv(T, CH)) * ft;
 #define AD(COND_, CALL_) if (COND_) return CALL_
   if (o == Orient::kSwap) {
-    AD(bn == 16, (launch_gemm<true, 16, kEpi, 10, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
-    AD(bn == 32, (launch_gemm<true, 32, kEpi, 9, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
-    AD(bn == 64, (launch_gemm<true, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 16, (launch_gemm<true, 16, kEpi, 10, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
+    AD(bn == 32, (launch_gemm<true, 32, kEpi, 9, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
+    AD(bn == 64, (launch_gemm<true, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
   } else if (o == Orient::kPair) {
-    AD(bn == 256, (launch_gemm_pair<256, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 256, (launch_gemm_pair<256, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
   } else {
-    AD(bn == 256, (launch_gemm<false, 256, kEpi, 4, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
-    AD(bn == 128, (launch_gemm<false, 128, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
-    AD(bn == 64, (launch_gemm<false, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops)));
+    AD(bn == 256, (launch_gemm<false, 256, kEpi, 4, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
+    AD(bn == 128, (launch_gemm<false, 128, kEpi, 6, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
+    AD(bn == 64, (launch_gemm<false, 64, kEpi, 8, GemmAdapt>(x, T, w, p.Nw, p, tiles, st, &ops, before)));
   }
 #undef AD
   return MOE_ERR_UNSUPPORTED;

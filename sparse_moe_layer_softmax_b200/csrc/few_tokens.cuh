@@ -125,6 +125,7 @@ struct FewTables {
   int expert[kFewSlots];               // ascending
   int count[kFewSlots];                // slots routed to that expert (at most T)
   uint8_t slot[kFewSlots][kFewTokens]; // those slots, in token order
+  uint8_t token[kFewSlots][kFewTokens]; // and their tokens
   int own[kMaxExperts / 32], most[kMaxExperts / 32];  // per group of 32 experts
   // adapters: the distinct ones the tokens use, and each token's (-1: none)
   int ndist_ad;
@@ -201,7 +202,23 @@ struct FewTiles {
                                  int valid = kFewRows, int half = 0) {
     return FewTile{map, row, half, K, K, valid, kind, r0, e};
   }
-  __device__ FewTile get(int phase, int i) const {
+  // The expert that tile i of an expert stage belongs to: `q` and its first tile `q0` follow i, which
+  // mostly goes up by one.
+  __device__ FewTile get_expert(int phase, int i, int per, int& q, int& q0) const {
+    if (i < q0 || i >= q0 + 2 * per) {
+      q = i / per;
+      q0 = q * per;
+    } else if (i >= q0 + per) {
+      ++q;
+      q0 += per;
+    }
+    const int j = i - q0, e = tb.expert[q];
+    if (phase == FEW_DOWN2) return tile(&m.w_down, e * p.E + j * 16, p.H, FEW_EXPERT_OUT, j * 16, q);
+    if (p.swiglu) return tile(&m.gate_up, j * 8, p.E, FEW_GATEUP, j * 8, q, kFewRows, 2 * e);
+    return tile(&m.gate_up, e * p.H + j * 16, p.E, FEW_GATEUP, j * 16, q);
+  }
+  __device__ FewTile get(int phase, int i, int per, int& q, int& q0) const {
+    if (phase == FEW_UP1 || phase == FEW_DOWN2) return get_expert(phase, i, per, q, q0);
     if (phase == FEW_IN) {
       const int nr = (p.n + 15) / 16, na = tb.ndist_ad * ad_tiles();
       if (i < nr) {
@@ -213,16 +230,10 @@ struct FewTiles {
       const int r0 = (i - nr - na) * 16;
       return tile(&m.p_down, r0, p.d, FEW_LATENT, r0);
     }
-    if (phase == FEW_OUT) {
-      const int na = tb.ndist_ad * ad_tiles();
-      if (i < na) return ad_tile(&m.ad_up, i, p.L, FEW_AD_UP);
-      const int r0 = (i - na) * 16;
-      return tile(&m.p_up, r0, p.L, FEW_LAYER_OUT, r0);
-    }
-    const int per = per_expert(phase), q = i / per, j = i - q * per, e = tb.expert[q];
-    if (phase == FEW_DOWN2) return tile(&m.w_down, e * p.E + j * 16, p.H, FEW_EXPERT_OUT, j * 16, q);
-    if (p.swiglu) return tile(&m.gate_up, j * 8, p.E, FEW_GATEUP, j * 8, q, kFewRows, 2 * e);
-    return tile(&m.gate_up, e * p.H + j * 16, p.E, FEW_GATEUP, j * 16, q);
+    const int na = tb.ndist_ad * ad_tiles();
+    if (i < na) return ad_tile(&m.ad_up, i, p.L, FEW_AD_UP);
+    const int r0 = (i - na) * 16;
+    return tile(&m.p_up, r0, p.L, FEW_LAYER_OUT, r0);
   }
   __device__ FewTile ad_tile(const CUtensorMap* map, int i, int K, int kind) const {
     const int q = i / ad_tiles(), r0 = (i - q * ad_tiles()) * 16;
@@ -548,7 +559,9 @@ __device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, vol
       tb.expert[at] = g * 32 + lane;
       tb.count[at] = cnt;
       for (int q = 0; q < cnt; ++q) {
-        tb.slot[at][q] = static_cast<uint8_t>(__ffsll(hits[i]) - 1);
+        const int slot = __ffsll(hits[i]) - 1;
+        tb.slot[at][q] = static_cast<uint8_t>(slot);
+        tb.token[at][q] = static_cast<uint8_t>(slot / p.k);
         hits[i] &= hits[i] - 1ull;
       }
     }
@@ -569,37 +582,54 @@ __device__ __forceinline__ void few_route(const FewParams& p, FewTables& tb, vol
   if (tid == 0) mbar_arrive(routed);
 }
 
-// A role's place in the ring: chunk c of the CTA's stream lies in stage (c - c0) % S, and warp
-// (c - c0) % W multiplies it.  The ring changes its depth between the dense and the expert stages (the
-// dense ones hold every token's row, the expert ones as many as one expert has); `bits` holds the
-// parity of the fills each stage had before.
+// A role's place in the ring: chunk c of a stage of the layer lies in ring stage c % S, and warp c % W
+// multiplies it.  The ring changes its depth between the dense and the expert stages (the dense ones hold
+// every token's row, the expert ones as many as one expert has); `bits` holds the parity of the fills
+// each ring stage had before.  Kept as running values: a division by S or W for every chunk and tile, with
+// those that found the tile, made a tile of small rows cost 0.95 us.
 struct FewRing {
-  unsigned S, W, c0 = 0, bits = 0, c = 0;
+  int S, W;
+  int stage = 0, turn = 0;       // of the next chunk
+  unsigned parity = 0, bits = 0; // of the fills since the last resize, and before it
   __device__ FewRing(int s, int w) : S(s), W(w) {}
-  __device__ void at(unsigned chunk, unsigned& stage, unsigned& parity) const {
-    const unsigned q = (chunk - c0) / S;
-    stage = (chunk - c0) - q * S;
-    parity = (bits >> stage ^ q) & 1u;
+  // ring stage and parity of the chunk `ahead` after the next
+  __device__ void at(int ahead, int& st, unsigned& par) const {
+    st = stage + ahead;
+    par = parity;
+    while (st >= S) {
+      st -= S;
+      par ^= 1u;
+    }
+    par = (par ^ bits >> st) & 1u;
+  }
+  __device__ void advance(int chunks) {
+    stage += chunks;
+    while (stage >= S) {
+      stage -= S;
+      parity ^= 1u;
+    }
+    turn += chunks;
+    while (turn >= W) turn -= W;
   }
   __device__ void resize(int s, int w) {
-    const unsigned q = (c - c0) / S, r = (c - c0) - q * S;
-    if (q & 1u) bits ^= (1u << S) - 1u;
-    bits ^= (1u << r) - 1u;
-    c0 = c;
+    if (parity & 1u) bits ^= (1u << S) - 1u;
+    bits ^= (1u << stage) - 1u;
+    stage = turn = 0;
+    parity = 0;
     S = s;
     W = w;
   }
 };
 
 // `rows` rows of K fp32 values from global memory into the activation region, by `threads` threads of
-// which this is number `id`.  Row r comes from source row slots[r] / div, or r without slots.  Four loads
+// which this is number `id`.  Row r comes from source row from_rows[r], or r without them.  Four loads
 // a thread are in flight: one by one, each took its 0.5 us or more (eight tokens' y: 9 us).
 template <bool kF32>
 __device__ __forceinline__ void few_load_rows(FewAct act, int id, int threads, int rows, int K, const float* src,
-                                           const uint8_t* slots, int div, const float* gain) {
+                                           const uint8_t* from_rows, const float* gain) {
   const int vec = K / 4;
   for (int row = 0; row < rows; ++row) {
-    const int from_row = slots ? slots[row] / div : row;
+    const int from_row = from_rows ? from_rows[row] : row;
     const float4* from = reinterpret_cast<const float4*>(src + static_cast<size_t>(from_row) * K);
     for (int i = id; i < vec; i += 4 * threads) {
       float4 v[4];
@@ -773,8 +803,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     bool ok = true;
     auto issue = [&](const FewTile& t) {
       for (int kb = 0; kb < t.K / kCols && ok; kb += kFewBlocks) {
-        unsigned stage, parity;
-        rg.at(rg.c++, stage, parity);
+        int stage;
+        unsigned parity;
+        rg.at(0, stage, parity);
+        rg.advance(1);
         if (!mbar_wait(&empty[stage], parity ^ 1u)) { ok = false; break; }
         mbar_arrive_expect_tx(&full[stage], kFewStageBytes);
         tma_load_4d(t.map, &full[stage], ring + stage * kFewStageBytes, 0, t.row, t.half, kb, policy);
@@ -797,7 +829,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       unsigned* counter = p.bar + (ph == FEW_UP1 ? 7 : 8) * 16;
       // a counter's answer takes about a tile's time to come: it is asked for one tile ahead
       int next = fixed < N ? static_cast<int>(atomicAdd(counter, 1u)) : N;
-      for (; i < end && ok; i += step) issue(tiles.get(ph, i));
+      const int per = tiles.per_expert(ph);
+      int eq = 0, eq0 = 0;
+      for (; i < end && ok; i += step) issue(tiles.get(ph, i, per, eq, eq0));
       while (fixed < N && ok) {
         const int j = fixed + next < N ? fixed + next : -1;
         if (j >= 0) next = static_cast<int>(atomicAdd(counter, 1u));
@@ -807,7 +841,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_arrive(&tq_full[q]);
         ++qn;
         if (j < 0) break;
-        issue(tiles.get(ph, j));
+        issue(tiles.get(ph, j, per, eq, eq0));
       }
     }
     if (!ok) *abort_ = 1;
@@ -880,7 +914,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       if (p.L) act = few_act<kF32>(act_mem, tb.rows, p.E, true);
       if (mma) {
         if (p.L && p.resident)
-          few_load_rows<kF32>(act, tid, kFewMma, T, p.E, p.z, nullptr, 1, p.pre_norm ? p.gamma_pre : nullptr);
+          few_load_rows<kF32>(act, tid, kFewMma, T, p.E, p.z, nullptr, p.pre_norm ? p.gamma_pre : nullptr);
         few_bar<FEW_MMA>();
       } else if (p.pre_norm) {
         for (int t = warp - kFewMmaWarps; t < T; t += kFewEpiWarps) {
@@ -904,7 +938,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       rg.resize(p.stages, p.turns);
       act_mem = ring + p.stages * kFewStageBytes;
       act = few_act<kF32>(act_mem, T, p.L, true);
-      few_load_rows<kF32>(act, tid, kFewWork, T, p.L, p.y, nullptr, 1, nullptr);
+      few_load_rows<kF32>(act, tid, kFewWork, T, p.L, p.y, nullptr, nullptr);
       few_bar<FEW_WORK>();
     }
 
@@ -914,6 +948,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int lead = expert ? 0 : tiles.lead_tiles(ph), lead_bar = ph == FEW_IN ? 0 : 5;
     bool lead_done = expert || (ph == FEW_OUT && tb.ndist_ad == 0), have_v = tb.ndist_ad == 0;
     int loaded = -1;
+    const int per = tiles.per_expert(ph);
+    int eq = 0, eq0 = 0;
     int i, end, step;
     tiles.range(ph, i, end, step);
     for (;; i += step) {
@@ -928,7 +964,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ++qn;
         if (j < 0) break;
       }
-      const FewTile t = tiles.get(ph, j);
+      const FewTile t = tiles.get(ph, j, per, eq, eq0);
       const int m = expert ? tb.count[t.e] : T;  // activation rows of this tile
       const unsigned rb = tile_no % kFewRedBufs, rturn = tile_no / kFewRedBufs & 1u;
       ++tile_no;
@@ -942,19 +978,19 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         if (per_expert && t.e != loaded) {  // its rows, once every warp is past the previous ones
           few_bar<FEW_MMA>();
           const bool up1 = ph == FEW_UP1;
-          few_load_rows<kF32>(act, tid, kFewMma, m, up1 ? p.E : p.H, up1 ? p.z : p.a, tb.slot[t.e], up1 ? k : 1,
-                              up1 && p.pre_norm ? p.gamma_pre : nullptr);
+          few_load_rows<kF32>(act, tid, kFewMma, m, up1 ? p.E : p.H, up1 ? p.z : p.a,
+                              up1 ? tb.token[t.e] : tb.slot[t.e], up1 && p.pre_norm ? p.gamma_pre : nullptr);
           few_bar<FEW_MMA>();
           loaded = t.e;
         }
-        const int W = static_cast<int>(rg.W), turn0 = static_cast<int>((rg.c - rg.c0) % rg.W);
+        const int W = rg.W, turn0 = rg.turn;
         const int first = warp - turn0 + (warp < turn0 ? W : 0);
         const bool part = warp < W && first < nch;
         float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
         if (part) {
           const uint32_t abase = smem_u32(act.base);
           auto row_at = [&](int c) {  // activation row of column c
-            const int row = ph == FEW_UP1 && !per_expert ? tb.slot[t.e][c] / k : c;
+            const int row = ph == FEW_UP1 && !per_expert ? tb.token[t.e][c] : c;
             return abase + static_cast<uint32_t>(row * act.pitch);
           };
           uint32_t xa = 0, xb = 0;
@@ -972,8 +1008,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             }
           }
           for (int ci = first; ci < nch; ci += W) {
-            unsigned stage, parity;
-            rg.at(rg.c + ci, stage, parity);
+            int stage;
+            unsigned parity;
+            rg.at(ci, stage, parity);
             if (!*abort_ && !mbar_wait(&full[stage], parity)) *abort_ = 1;
             const uint32_t st = smem_u32(ring) + stage * kFewStageBytes;
             const int k0 = ci * kPer, kw = min(kPer, t.K - k0);
@@ -997,7 +1034,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&red_full[rb]);
-        rg.c += nch;
+        rg.advance(nch);
         continue;
       }
 
@@ -1025,7 +1062,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       float v = 0.0f, up = 0.0f;
       {
         const float* at = red + rb * kFewRedFloats + row * kFewRedPitch + min(col, kFewTokens - 1);
-        const int parts = min(nch, static_cast<int>(rg.W));
+        const int parts = min(nch, rg.W);
         for (int q = 0; q < parts; ++q, at += kFewRows * kFewRedPitch) {
           v += at[0];
           if (dual) up += at[8 * kFewRedPitch];
@@ -1062,7 +1099,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         case FEW_GATEUP:
           if (mine) {
             const int slot = tb.slot[t.e][col];
-            const float inv = p.pre_norm ? tb.norm[slot / k] : 1.0f;
+            const float inv = p.pre_norm ? tb.norm[tb.token[t.e][col]] : 1.0f;
             v *= inv;
             if (dual) v = v / (1.0f + expf(-v)) * (up * inv);
             else v = v < 0.0f ? 0.0f : v;  // NaN stays NaN (fmaxf would drop it)

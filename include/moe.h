@@ -340,7 +340,8 @@ MOE_API moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_w
  *   - workspace: moe_adapters_workspace_size bytes (host arithmetic; grows with T * min(n_adapters,
  *     256) * 128 bytes), contents need not be initialised.  Calls that share it must not overlap.
  *   - Outputs must not alias inputs.  Errors as for moe_latent_down / moe_latent_up, and
- *     MOE_ERR_UNSUPPORTED for a rank that is no multiple of 8 or above MOE_ADAPTER_MAX_RANK. */
+ *     MOE_ERR_UNSUPPORTED for a rank that is no multiple of 8 or above MOE_ADAPTER_MAX_RANK, or for
+ *     more adapters than 2^31 rows of their stacked matrices. */
 MOE_API moe_status_t moe_adapters_workspace_size(const moe_config_t* cfg,
                                                  const moe_adapters_t* adapters, size_t* bytes);
 MOE_API moe_status_t moe_latent_down_adapters(const moe_config_t* cfg, const void* u,
@@ -373,8 +374,8 @@ MOE_API moe_status_t moe_layer_forward_adapters(const moe_config_t* cfg, const m
  *     each to bf16); only out is rounded.  With input_norm, u is rounded to bf16 as in the batch path.
  *     Results are deterministic, and within the batch path's rounding of moe_layer_forward's.
  *   - Widths are multiples of 64 (bf16) or 32 (fp32).  The activations of one stage must fit in
- *     shared memory beside the weight ring, at most about 172 KB: T * d_model * 2 bytes and
- *     T * 4 * max(d_latent, d_ff) bytes (bf16; fp32: T * 4 * max(d_model, d_ff)).  Otherwise, and for
+ *     shared memory beside the weight ring, about 148 KB: T * d_model * 2 bytes and T * 4 *
+ *     max(d_latent, d_ff) bytes (bf16; fp32: T * 4 * max(d_model, d_ff)).  Otherwise, and for
  *     T > MOE_FEW_MAX_TOKENS, MOE_ERR_UNSUPPORTED: use moe_layer_forward.
  *   - workspace: moe_few_workspace_size bytes (host arithmetic; adapters as in the call).  Its contents
  *     need not be initialised.  Calls that share a workspace must not overlap on the GPU.

@@ -361,7 +361,9 @@ def _check_adapter_shapes(cfg, adapters, token_adapter, pairs):
     if token_adapter is None or token_adapter.dtype != torch.int32 or \
             token_adapter.numel() != cfg.T or not token_adapter.is_contiguous():
         raise ValueError("token_adapter: a contiguous int32 tensor with one entry per token")
-    for name, t in getattr(adapters, "tensors", {}).items():
+    if token_adapter.device != adapters.tensors["scale"].device:
+        raise ValueError("token_adapter and the adapters are on different devices")
+    for name, t in adapters.tensors.items():
         if name.rsplit("_", 1)[0] not in pairs or t is None:
             continue
         want = {"down_a": (2, cfg.d_model), "down_b": (1, cfg.d_latent), "up_a": (2, cfg.d_latent),

@@ -9,12 +9,16 @@
 //
 // What bounds it: at this size the layer is a stream of weights, each read once (944 MB for one
 // token of the Muse layer, about 5.9 GB for eight), with one multiply-add per weight and token.
+// Measured: one token 160 us, 0.90 of what its bytes take at the measured copy rate (the batch path, eight
+// launches: 200 us); eight tokens 842 us (874), the expert stages at 7.0-7.2 TB/s.  What is left at one
+// token are the pauses between the stages: the selection (4 us), two exchanges of 64 KB and less through
+// L2 per expert stage (3 us each, in which the ring fills), launch and last tiles.
 // So everything is arranged around that stream never pausing:
 //   - One CTA per SM.  A producer thread walks this CTA's weight tiles of every stage of the layer in
-//     order and copies them into one shared-memory ring by TMA, 16 KB a box (bulk copies of one row
-//     each, 1 KB, reached 2.9 TB/s: the copy engine takes them one by one); it never waits for the
+//     order and copies them into one shared-memory ring by TMA, 16 KB a box; it never waits for the
 //     arithmetic of a stage, only for ring slots and, once, for the routing.  While the CTAs wait
-//     for one another between stages, the ring fills with the next stage's weights.
+//     for one another between stages, the ring fills with the next stage's weights.  Deeper than 128 KB
+//     the ring only lengthens the queue that the exchanges between the stages stand in (192 KB: 171 us).
 //   - A tile is 16 weight rows; eight warps share its reduction, each accumulating with m16n8k16
 //     tensor-core products: 16 weight rows on M and the tokens on N = 8.  The stream asks for
 //     one such instruction per SM about every 12 clocks, far below what the warp-level tensor path
@@ -51,7 +55,6 @@ constexpr int kFewRows = 16;                   // weight rows per tile
 constexpr int kFewBlocks = 8;                  // k-blocks (128 bytes of a row) per stage
 constexpr int kFewStageBytes = kFewBlocks * kFewRows * 128;
 constexpr int kFewMaxStages = 8;
-constexpr int kFewMaxRank = 128;
 constexpr int kFewRedPitch = 10;               // floats per row of a partial tile (no bank conflicts)
 constexpr int kFewRedFloats = kFewMmaWarps * kFewRows * kFewRedPitch;
 constexpr int kFewRedBufs = 2;
@@ -342,7 +345,7 @@ __device__ __forceinline__ void few_act_put4(const FewAct& a, int row, int c, fl
 __device__ __forceinline__ int few_row(int g) { return (g >> 1) + 4 * (g & 1); }
 
 // 16 bytes at a shared-memory address.  (Loads through pointers into the aligned ring would be generic
-// ones, twice the latency: the layer at eight tokens ran at 4.1 TB/s with them.)
+// ones of twice the latency.)
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
   uint4 v;
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
@@ -661,6 +664,7 @@ __device__ __forceinline__ void few_load_u(const FewParams& p, FewAct act, int t
 #pragma unroll 4
     for (int i = tid; i < vec; i += kFewWork) *reinterpret_cast<uint4*>(dst + i * 16) = row[i];
   }
+  fence_proxy_async_smem();  // the ring may grow into this place
   few_bar<FEW_WORK>();
   if constexpr (!kF32) {
     if (p.input_norm) {
@@ -820,6 +824,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         ok = mbar_wait(&routed, 0);
         rg.resize(tb.stages, tb.turns);
       } else if (ph == FEW_OUT) {
+        // Where this ring is the deeper one, its further stages lie in the expert stages' activations.  They
+        // are filled after all the others, each of which is free only once its last chunk of the expert
+        // stages has been multiplied: nothing reads those activations any more.
         rg.resize(p.stages, p.turns);
       }
       if (!ok) break;

@@ -994,6 +994,9 @@ moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, con
   if (c.dtype != MOE_BF16 || c.d_latent == 0) return MOE_ERR_UNSUPPORTED;
   if (ad->n_adapters <= 0 || ad->rank <= 0) return MOE_ERR_INVALID_ARG;
   if (ad->rank % 8 || ad->rank > MOE_ADAPTER_MAX_RANK) return MOE_ERR_UNSUPPORTED;
+  // rows of the stacked matrices are counted in 32 bits
+  const long widest = std::max({c.d_model, c.d_latent, static_cast<int32_t>(MOE_ADAPTER_MAX_RANK)});
+  if (ad->n_adapters > 0x7fffffffL / widest) return MOE_ERR_UNSUPPORTED;
   if (c.T == 0) return MOE_OK;
   if (!ad->scale || !which) return MOE_ERR_INVALID_ARG;
   if (down && (!ad->down_a || !ad->down_b)) return MOE_ERR_INVALID_ARG;
@@ -1140,13 +1143,13 @@ FewLayout few_layout(const moe_config_t& c, int rank) {
   // dense stages: u (and y) of every token; without latent projections u stays through the experts
   size_t dense = T * row(d);
   if (c.d_latent > 0) dense = std::max(dense, planes * T * row(E));
-  const size_t expert = planes * T * std::max(row(E), row(H));  // if one expert has every token
+  // expert stages: z (latent layers) or the hidden values of one expert's tokens, at most all of them
+  const size_t wide = c.d_latent > 0 ? std::max(row(E), row(H)) : row(H), expert = planes * T * wide;
   const size_t rest = 1024 + kFewRedBufs * kFewRedFloats * 4 + align_up(T * rank * 4, 16);  // 1024: alignment
   if (std::max(dense, expert) + rest > static_cast<size_t>(kFewSmem)) return L;
   L.pool_bytes = static_cast<int>((kFewSmem - rest) / 1024 * 1024);
   for (size_t rows = 1; rows <= T; ++rows)
-    few_ring(L.pool_bytes - static_cast<int>(planes * rows * std::max(row(E), row(H))), &L.ring_stages[rows],
-             &L.ring_turns[rows]);
+    few_ring(L.pool_bytes - static_cast<int>(planes * rows * wide), &L.ring_stages[rows], &L.ring_turns[rows]);
   if (L.ring_stages[T] == 0) return L;
   // every token's z stays in shared memory through the first expert stage where that leaves the ring
   // its full depth

@@ -105,7 +105,8 @@ def test_adapted_projections_mixes(T, mix):
 
 def test_adapted_projections_full_width():
     """The Muse widths: a decode batch, a small prompt and a prefill batch."""
-    for T, nA, rank, mix in ((1, 4, 16, "each"), (64, 64, 16, "each"), (300, 16, 8, "any"), (3000, 8, 32, "packed")):
+    for T, nA, rank, mix in ((1, 4, 16, "each"), (64, 64, 16, "each"), (50, 5, 128, "any"), (64, 64, 128, "each"),
+                               (300, 16, 8, "any"), (3000, 8, 32, "packed")):
         check_both(T, 8192, 4096, nA, rank, mix, seed=T)
 
 

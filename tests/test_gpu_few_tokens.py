@@ -112,6 +112,18 @@ def test_few_every_token_on_the_same_experts():
     close(c, out, ref.layer(c, w, u, u)[0])
 
 
+@pytest.mark.parametrize("T,d,L,I", [(8, 4096, 2048, 4096), (7, 2048, 2048, 3392), (8, 64, 128, 3392), (6, 8192, 512, 4096)])
+def test_few_wide_hidden_layers_with_every_token_on_one_expert(T, d, L, I):
+    """The expert stages hold more activations than the dense ones, and the way up's weights are on their
+    way while the last expert still multiplies."""
+    c = dict(MUSE, T=T, d=d, L=L, I=I, n=8, k=2)
+    w, u, gen = ref.make_layer(c, 32)
+    w["logit_bias"] = torch.zeros(8, device="cuda")
+    w["logit_bias"][[2, 5]] = 100.0
+    for _ in range(3):
+        close(c, run_few(c, w, u)[0], ref.layer(c, w, u, u)[0])
+
+
 def test_few_repeats_bit_for_bit_on_any_workspace():
     c = dict(MUSE, T=8)
     w, u, gen = ref.make_layer(c, 23)

@@ -1,0 +1,161 @@
+"""The few-token layer and the adapted projections without a GPU: their refusals, all of them made on the
+host before anything is launched, and the host arithmetic of their workspaces."""
+import ctypes
+
+import pytest
+
+import sparse_moe_layer_softmax_b200 as moe
+from sparse_moe_layer_softmax_b200 import build as moe_build
+
+CODE = moe.STATUS_CODES
+A = 0x10000  # a 16-byte aligned address that no call gets as far as using
+
+
+@pytest.fixture(scope="module")
+def lib():
+    moe_build.build()
+    return moe.lib()
+
+
+def muse(**kw):
+    base = dict(T=4, d_model=512, n_experts=32, top_k=4, d_ff=256, d_latent=256, pre_norm=1, expert_norm=1,
+                resid_mode=moe.MOE_RESID_MUSE_GATE)
+    return moe.make_config(**{**base, **kw})
+
+
+def weights(**kw):
+    return moe.Weights(**{**dict.fromkeys((f for f, _ in moe.Weights._fields_), A), **kw})
+
+
+def adapters(**kw):
+    return moe.Adapters(**{**dict(n_adapters=3, rank=16, down_a=A, down_b=A, up_a=A, up_b=A, scale=A), **kw})
+
+
+def few(lib, c, w=None, ad=None, which=None, u=A, r=A, out=A, idx=None, ws=A, size=1 << 40):
+    return lib.moe_layer_forward_few(ctypes.byref(c), ctypes.byref(w or weights()),
+                                     ctypes.byref(ad) if ad else None, which, u, r, out, None, idx, None, ws, size,
+                                     None)
+
+
+def down(lib, c, ad, which=A, u=A, p=A, z=A, ws=A, size=1 << 40):
+    return lib.moe_latent_down_adapters(ctypes.byref(c), u, p, ctypes.byref(ad) if ad else None, which, z, ws, size,
+                                        None)
+
+
+def up(lib, c, ad, which=A, y=A, p=A, r=A, g=A, out=A, ws=A, size=1 << 40):
+    return lib.moe_latent_up_adapters(ctypes.byref(c), y, p, ctypes.byref(ad) if ad else None, which, r, g, out, ws,
+                                      size, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(T=9), "MOE_ERR_UNSUPPORTED"), (dict(T=-1), "MOE_ERR_INVALID_ARG"),
+    (dict(d_model=100), "MOE_ERR_UNSUPPORTED"), (dict(top_k=9), "MOE_ERR_UNSUPPORTED"),
+    (dict(n_experts=257), "MOE_ERR_UNSUPPORTED"),
+    (dict(T=8, d_ff=8192), "MOE_ERR_UNSUPPORTED"),  # activations beyond shared memory
+    (dict(T=8, d_latent=8192, d_model=8192), "MOE_ERR_UNSUPPORTED"),
+    (dict(T=8, d_model=16384), "MOE_ERR_UNSUPPORTED"),
+    (dict(dtype=moe.MOE_F32, d_latent=0, pre_norm=0, resid_mode=0, d_model=40), "MOE_ERR_UNSUPPORTED"),
+    (dict(dtype=moe.MOE_F32, d_latent=0, pre_norm=0, resid_mode=0, d_ff=48), "MOE_ERR_UNSUPPORTED"),
+])
+def test_few_refuses_configurations(lib, kw, code):
+    c = muse(**kw)
+    n = ctypes.c_size_t()
+    assert lib.moe_few_workspace_size(ctypes.byref(c), None, ctypes.byref(n)) == CODE[code]
+    assert few(lib, c) == CODE[code]
+
+
+def test_few_refuses_arguments(lib):
+    c = muse()
+    n = moe.few_workspace_size(c)
+    assert 0 < n < 1 << 20
+    assert few(lib, c, ws=None) == CODE["MOE_ERR_WORKSPACE"]
+    assert few(lib, c, size=n - 1) == CODE["MOE_ERR_WORKSPACE"]
+    assert few(lib, c, u=None) == CODE["MOE_ERR_INVALID_ARG"]
+    assert few(lib, c, out=None) == CODE["MOE_ERR_INVALID_ARG"]
+    assert few(lib, c, r=None) == CODE["MOE_ERR_INVALID_ARG"]
+    assert few(lib, c, u=A + 2) == CODE["MOE_ERR_ALIGNMENT"]
+    assert few(lib, c, idx=A + 4) == CODE["MOE_ERR_ALIGNMENT"]
+    assert few(lib, c, w=weights(w_gu=None)) == CODE["MOE_ERR_INVALID_ARG"]
+    assert few(lib, c, w=weights(gamma_pre=None)) == CODE["MOE_ERR_INVALID_ARG"]
+    assert few(lib, c, w=weights(resid_g=A + 4)) == CODE["MOE_ERR_ALIGNMENT"]
+    assert few(lib, muse(T=0), u=None, r=None, out=None, ws=None, size=0) == CODE["MOE_OK"]
+    assert lib.moe_few_workspace_size(ctypes.byref(c), None, None) == CODE["MOE_ERR_INVALID_ARG"]
+    # the Muse layer at its full widths fits for every number of tokens, with the largest adapters too
+    for T in range(1, 9):
+        full = muse(T=T, d_model=8192, d_latent=4096, d_ff=4096, n_experts=256, top_k=8)
+        assert moe.few_workspace_size(full, adapters(rank=128)) > moe.few_workspace_size(full)
+
+
+ADAPTER_FAULTS = [
+    (dict(n_adapters=0), "MOE_ERR_INVALID_ARG"), (dict(n_adapters=-2), "MOE_ERR_INVALID_ARG"),
+    (dict(rank=0), "MOE_ERR_INVALID_ARG"), (dict(rank=-8), "MOE_ERR_INVALID_ARG"),
+    (dict(rank=12), "MOE_ERR_UNSUPPORTED"), (dict(rank=136), "MOE_ERR_UNSUPPORTED"),
+    (dict(n_adapters=1 << 23), "MOE_ERR_UNSUPPORTED"),
+    (dict(scale=None), "MOE_ERR_INVALID_ARG"), (dict(scale=A + 4), "MOE_ERR_ALIGNMENT"),
+    (dict(down_a=None), "MOE_ERR_INVALID_ARG"), (dict(down_b=A + 8), "MOE_ERR_ALIGNMENT"),
+]
+
+
+@pytest.mark.parametrize("kw,code", ADAPTER_FAULTS)
+@pytest.mark.parametrize("T", [4, 300])
+def test_adapters_are_checked(lib, kw, code, T):
+    c, ad = muse(T=T), adapters(**kw)
+    assert down(lib, c, ad) == CODE[code]
+    if T <= 8:
+        assert few(lib, c, ad=ad, which=A) == CODE[code]
+    n = ctypes.c_size_t()
+    size = lib.moe_adapters_workspace_size(ctypes.byref(c), ctypes.byref(ad), ctypes.byref(n))
+    assert size == (CODE[code] if set(kw) & {"n_adapters", "rank"} else CODE["MOE_OK"])
+    whole = lib.moe_layer_forward_adapters(ctypes.byref(c), ctypes.byref(weights()), ctypes.byref(ad), A, A, A, A,
+                                           None, None, None, A, 1 << 40, None)
+    assert whole == CODE[code]
+
+
+def test_adapted_projections_refuse_arguments(lib):
+    c, ad = muse(T=70), adapters()
+    n = moe.adapters_workspace_size(c, ad)
+    for f, first in ((down, "u"), (up, "y")):
+        assert f(lib, c, None) == CODE["MOE_ERR_INVALID_ARG"]
+        assert f(lib, c, ad, which=None) == CODE["MOE_ERR_INVALID_ARG"]
+        assert f(lib, c, ad, which=A + 2) == CODE["MOE_ERR_ALIGNMENT"]
+        assert f(lib, c, ad, which=A + 4, size=0) == CODE["MOE_ERR_WORKSPACE"]  # 4 bytes are enough for it
+        assert f(lib, c, ad, **{first: None}) == CODE["MOE_ERR_INVALID_ARG"]
+        assert f(lib, c, ad, p=A + 4) == CODE["MOE_ERR_ALIGNMENT"]
+        assert f(lib, c, ad, ws=None) == CODE["MOE_ERR_WORKSPACE"]
+        assert f(lib, c, ad, size=n - 1) == CODE["MOE_ERR_WORKSPACE"]
+        assert f(lib, muse(T=0), ad, which=None, ws=None, size=0) == CODE["MOE_OK"]
+        plain = muse(d_latent=0, pre_norm=0, resid_mode=0)
+        assert f(lib, plain, ad) == CODE["MOE_ERR_UNSUPPORTED"]  # no latent projections
+    assert up(lib, c, ad, r=None) == CODE["MOE_ERR_INVALID_ARG"]
+    # each projection asks for its own pair only
+    assert down(lib, c, adapters(up_a=None, up_b=None), size=0) == CODE["MOE_ERR_WORKSPACE"]
+    assert up(lib, c, adapters(down_a=None, down_b=None), size=0) == CODE["MOE_ERR_WORKSPACE"]
+    # the whole layer needs both workspaces
+    whole = lib.moe_layer_forward_adapters(ctypes.byref(c), ctypes.byref(weights()), ctypes.byref(ad), A, A, A, A,
+                                           None, None, None, A, moe.workspace_size(c) + n - 1, None)
+    assert whole == CODE["MOE_ERR_WORKSPACE"]
+
+
+def test_adapter_workspace_is_host_arithmetic(lib):
+    ad = adapters(n_adapters=64)
+    sizes = [moe.adapters_workspace_size(muse(T=T, d_model=8192, d_latent=4096), ad) for T in (1, 64, 65, 2048, 16384)]
+    assert sizes == sorted(sizes) and sizes[-1] < 300 << 20
+
+
+def test_make_adapters_checks_shapes():
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    a = {"scale": torch.ones(2), "down_a": torch.zeros(2, 8, 64, dtype=bf), "down_b": torch.zeros(2, 128, 8, dtype=bf)}
+    ad = moe.make_adapters(a)
+    assert (ad.n_adapters, ad.rank, ad.up_a) == (2, 8, None)
+    for bad in (dict(a, scale=torch.ones(2, dtype=torch.float64)), dict(a, down_b=torch.zeros(2, 128, 16, dtype=bf)),
+                dict(a, down_a=torch.zeros(3, 8, 64, dtype=bf)), dict(a, down_a=torch.zeros(2, 8, 64)),
+                dict(a, down_a=a["down_a"].transpose(1, 2)), {"scale": torch.ones(2)}):
+        with pytest.raises(ValueError):
+            moe.make_adapters(bad)
+    cfg = muse(T=3, d_model=64, d_latent=128)
+    which = torch.zeros(3, dtype=torch.int32)
+    moe._check_adapter_shapes(cfg, ad, which, ("down",))
+    for args in ((muse(T=3, d_model=128, d_latent=128), which), (cfg, which.long()), (cfg, which[:2]), (cfg, None)):
+        with pytest.raises(ValueError):
+            moe._check_adapter_shapes(args[0], ad, args[1], ("down",))

@@ -34,6 +34,12 @@ constexpr int kAdGroupCols = 256;    // rows of A that one pass over the tokens 
 constexpr int kAdStages = 4;
 constexpr int kAdMaxSplits = 16;
 constexpr int kAdMaxChunk = 256;     // rows of the projection's largest tile
+// Columns of all adapters side by side, up to which a call lays them out so.  The copy moves at most 16 MB
+// each way, 5 us, beside the inner products; a tile of 46 adapters of rank 8 then takes 12 blocks instead of
+// 46 (2245 rows of 1664 values into 6720: 355 -> 220 us).  Each adapter has whole 16-column steps of the MMA,
+// so its sums, and every token's bits, are those of a block of its own.
+constexpr int kAdCatCols = 1024;
+__host__ __device__ constexpr int adapt_cat_rank(int rank) { return (rank + 15) / 16 * 16; }
 constexpr int kAdSlices = 8;         // parts of an adapter's B that are looked through apart
 constexpr int kAdStageBytes = kAdChunk * 128 + kAdGroupCols * 128;
 constexpr int kAdSmem = kAdStages * kAdStageBytes + 1024;
@@ -175,11 +181,14 @@ __device__ __forceinline__ bool bf16x8_nonfinite(const uint4& q) {
 }
 
 // Looks through the used adapters' B matrices, kAdSlices CTAs to an adapter: byte [a, slice] of bad is 1
-// if the slice holds a non-finite value.  Runs beside the inner products (where few of their threads
-// are free, the same work took up to 100 us).
+// if the slice holds a non-finite value.  kCat: it also lays the matrices side by side, cat[f, a rp + c] =
+// B[a, f, c], rp the rank rounded up to 16, with zeros for unused adapters, in place of non-finite values and
+// past the rank.  Runs beside the inner products (where few of their threads are free, the same work took up
+// to 100 us).
+template <bool kCat>
 __global__ void __launch_bounds__(256)
     adapter_check_kernel(const int32_t* __restrict__ which, int T, const uint16_t* __restrict__ B, long b_elems,
-                         uint8_t* __restrict__ bad) {
+                         uint8_t* __restrict__ bad, int rank, int cat_pitch, uint16_t* __restrict__ cat) {
   pdl_wait();
   pdl_launch_dependents();
   const int tid = threadIdx.x, a = static_cast<int>(blockIdx.x) / kAdSlices;
@@ -187,15 +196,27 @@ __global__ void __launch_bounds__(256)
   bool used = false;
 #pragma unroll 8
   for (int t = tid; t < T; t += 256) used = (which[t] == a) || used;
-  if (!__syncthreads_or(used)) return;
+  used = __syncthreads_or(used);
+  if (!used && !kCat) return;
   const long vecs = b_elems / 8, lo = vecs * slice / kAdSlices, hi = vecs * (slice + 1) / kAdSlices;
   const uint4* p = reinterpret_cast<const uint4*>(B + static_cast<size_t>(a) * b_elems);
+  const int row_vecs = rank / 8;
   bool found = false;
 #pragma unroll 8
   for (long j = lo + tid; j < hi; j += 256) {
-    const uint4 w = __ldg(p + j);
-    found = bf16x8_nonfinite(w) || found;
+    uint4 w = !kCat || used ? __ldg(p + j) : make_uint4(0, 0, 0, 0);
+    const bool broken = bf16x8_nonfinite(w);
+    found = broken || found;
+    if constexpr (kCat) {  // what an adapter that is left out holds does not matter, as long as it is finite
+      if (broken) w = make_uint4(0, 0, 0, 0);
+      const long f = j / row_vecs;
+      const int u = static_cast<int>(j - f * row_vecs);
+      uint4* at = reinterpret_cast<uint4*>(cat + f * cat_pitch + a * adapt_cat_rank(rank) + u * 8);
+      at[0] = w;
+      if (rank % 16 && u == row_vecs - 1) at[1] = make_uint4(0, 0, 0, 0);
+    }
   }
+  if (!used) return;
   found = __syncthreads_or(found);
   if (tid == 0) {
     bad[a * kAdSlices + slice] = found;
@@ -323,12 +344,13 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
 // The projection GEMM's operands, tile by tile of CH <= 256 rows: the adapters the rows use (without
 // those whose B is broken) and, per row, one block of rb * 64 columns for each of them: scale * v (the
-// splits added in order) in its own adapter's block, zeros in the others.  Each CTA finds its tile's
+// splits added in order) in its own adapter's block, zeros in the others.  Where the blocks of all
+// adapters side by side are fewer (all > 0), the rows are laid out over those.  Each CTA finds its tile's
 // adapters and writes `per` of its rows (one CTA a tile: 84 us for 333 rows in 3 tiles).
 __global__ void __launch_bounds__(kAdMaxChunk)
     adapter_pack_kernel(const float* __restrict__ v, int splits, int T, const int32_t* __restrict__ which,
                         int n, int rank, const float* __restrict__ scale,
-                        const unsigned long long* __restrict__ bad, int CH, int cap, int rb, int per,
+                        const unsigned long long* __restrict__ bad, int CH, int cap, int rb, int per, int all,
                         int* __restrict__ count, int* __restrict__ list, uint16_t* __restrict__ V) {
   __shared__ __align__(16) int s_ad[kAdMaxChunk];
   __shared__ int s_slot[kAdMaxChunk], s_list[kAdMaxChunk], s_cnt[9];
@@ -345,16 +367,19 @@ __global__ void __launch_bounds__(kAdMaxChunk)
   __syncthreads();
   const int ns = adapter_slots(s_ad, rows, s_slot, s_list, s_cnt);
   if (group == 0) {
-    if (tid == 0) count[tile] = ns;
+    if (tid == 0) count[tile] = all > 0 && ns * rb > all ? -1 : ns;
     if (tid < ns) list[tile * adapt_list_pitch(cap) + tid] = s_list[tid];
   }
   const int first = group * per, mine = min(per, rows - first);
-  const int vec = ns * rb * 8;  // 16-byte units of a row
+  const bool cat = all > 0 && ns * rb > all;
+  const int vec = (cat ? all : ns * rb) * 8;  // 16-byte units of a row
+  const int width = cat ? adapt_cat_rank(rank) / 8 : rb * 8;
   const size_t pitch = static_cast<size_t>(cap) * rb * 64;
   for (int i = tid; i < mine * vec; i += kAdMaxChunk) {
-    const int r = i / vec, row = first + r, u = i - r * vec, c = u % (rb * 8) * 8;
+    const int r = i / vec, row = first + r, u = i - r * vec;
+    const int block = u / width, c = (u - block * width) * 8;  // the adapter, or its slot
     uint4 o = make_uint4(0, 0, 0, 0);
-    if (u / (rb * 8) == s_slot[row] && c < rank) {
+    if (block == (cat ? s_ad[row] : s_slot[row]) && c < rank) {
       float f[8] = {};
 #pragma unroll 8
       for (int s = 0; s < splits; ++s) {

@@ -73,8 +73,11 @@ struct GemmParams {
 // Extension of a dense projection's reduction by low-rank adapters: row tile `chunk` multiplies, after
 // the K columns of X and W, count[chunk] * rblocks further blocks of 64: block (slot, rb) takes columns
 // (slot * rblocks + rb) * 64 of v's rows against columns rb * 64 of the tile's rows of adapter
-// list[chunk * cap + slot]'s matrix in b.  v, count and list come from the kernels just before this one,
-// which run on while X and W are multiplied: only the extension waits for them.
+// list[chunk * cap + slot]'s matrix in b.  A negative count: v's rows are laid out over all adapters, and
+// the extension takes their `all` blocks against columns of cat, where the adapters' matrices stand side by
+// side (for tiles of many adapters of small rank, 64 columns each would be mostly zeros).  v, count, list
+// and cat come from the kernels just before this one, which run on while X and W are multiplied: only the
+// extension waits for them.
 struct NoAdapt {
   static constexpr bool kOn = false;
 };
@@ -82,9 +85,11 @@ struct GemmAdapt {
   static constexpr bool kOn = true;
   CUtensorMap v;     // [rows, cap * rblocks * 64]
   CUtensorMap b;     // [n_adapters * Nout, rank]
+  CUtensorMap cat;   // [Nout, n_adapters * rank rounded up to 16] (all > 0)
   const int* count;
   const int* list;
-  int cap, rblocks;
+  int cap, rblocks, all;
+  __device__ int blocks(int n) const { return n < 0 ? all : n * rblocks; }  // of a tile of count n
 };
 // The k-block at which a tile's extension is looked up, so that the answer is there when it is needed.
 __device__ __forceinline__ int adapt_early(int KB) { return KB > 12 ? KB - 12 : 0; }
@@ -611,15 +616,18 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
       if constexpr (Adapt::kOn) {
-        for (int slot = 0; slot < adapters.slots && ok; ++slot) {
-          const int brow = adapters(slot) * p.Nw + c.ft * S::kFO;
-          for (int rb = 0; rb < ad.rblocks; ++rb) {
+        const bool cat = adapters.slots < 0;  // then one slot, of all adapters
+        const CUtensorMap* map = cat ? &ad.cat : &ad.b;
+        const int slots = cat ? 1 : adapters.slots, per = cat ? ad.all : ad.rblocks;
+        for (int slot = 0; slot < slots && ok; ++slot) {
+          const int brow = (cat ? 0 : adapters(slot) * p.Nw) + c.ft * S::kFO;
+          for (int rb = 0; rb < per; ++rb) {
             if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
             uint8_t* sa = tiles + stage * S::kStageBytes;
             uint8_t* sb = sa + S::kABytes;
             mbar_arrive_expect_tx(&full[stage], S::kStageBytes);
-            tma_load_2d(&ad.v, &full[stage], kSwap ? sb : sa, (slot * ad.rblocks + rb) * 64, c.row0);
-            tma_load_2d(&ad.b, &full[stage], kSwap ? sa : sb, rb * 64, brow);
+            tma_load_2d(&ad.v, &full[stage], kSwap ? sb : sa, (slot * per + rb) * 64, c.row0);
+            tma_load_2d(map, &full[stage], kSwap ? sa : sb, rb * 64, brow);
             issued[stage] = true;
             last_parity[stage] = phase;
             if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -666,7 +674,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if constexpr (Adapt::kOn) {
           if (kb == early) {  // the extension's length, known once the kernel before is done
             pdl_wait();
-            ext = __ldcg(&ad.count[chunk]) * ad.rblocks;
+            ext = ad.blocks(__ldcg(&ad.count[chunk]));
           }
           if (kb == KB - 1) blocks += ext;
         }
@@ -914,15 +922,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (++stage == kStages) { stage = 0; phase ^= 1; }
       }
       if constexpr (Adapt::kOn) {
-        for (int slot = 0; slot < adapters.slots && ok; ++slot) {
-          const int brow = adapters(slot) * p.Nw + c.ft * BN + static_cast<int>(rank) * (BN / 2);
-          for (int rb = 0; rb < ad.rblocks; ++rb) {
+        const bool cat = adapters.slots < 0;  // then one slot, of all adapters
+        const CUtensorMap* map = cat ? &ad.cat : &ad.b;
+        const int slots = cat ? 1 : adapters.slots, per = cat ? ad.all : ad.rblocks;
+        for (int slot = 0; slot < slots && ok; ++slot) {
+          const int brow = (cat ? 0 : adapters(slot) * p.Nw) + c.ft * BN + static_cast<int>(rank) * (BN / 2);
+          for (int rb = 0; rb < per; ++rb) {
             if (!mbar_wait(&empty[stage], phase ^ 1)) { ok = false; break; }
             uint8_t* sa = tiles + stage * S::kStageBytes;
             if (leader) mbar_arrive_expect_tx(&full[stage], 2 * S::kStageBytes);
             const uint32_t fb = cluster_addr(&full[stage], 0);
-            tma_load_2d_pair(&ad.v, fb, sa, (slot * ad.rblocks + rb) * 64, xrow);
-            tma_load_2d_pair(&ad.b, fb, sa + S::kABytes, rb * 64, brow);
+            tma_load_2d_pair(&ad.v, fb, sa, (slot * per + rb) * 64, xrow);
+            tma_load_2d_pair(map, fb, sa + S::kABytes, rb * 64, brow);
             issued[stage] = true;
             last_parity[stage] = phase;
             if (++stage == kStages) { stage = 0; phase ^= 1; }
@@ -960,7 +971,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if constexpr (Adapt::kOn) {
             if (kb == early) {
               pdl_wait();
-              ext = __ldcg(&ad.count[chunk]) * ad.rblocks;
+              ext = ad.blocks(__ldcg(&ad.count[chunk]));
             }
             if (kb == KB - 1) blocks += ext;
           }

@@ -148,7 +148,8 @@ struct AdaptOperands {
   const void* b;
   const int* count;
   const int* list;
-  int n, rank, cap, rblocks;
+  const void* cat;  // [Nout, n * rank rounded up to 16], or nullptr with all == 0
+  int n, rank, cap, rblocks, all;
 };
 bool make_adapt(NoAdapt*, const AdaptOperands*, long, const GemmParams&, uint32_t, uint32_t) { return true; }
 bool make_adapt(GemmAdapt* g, const AdaptOperands* o, long x_rows, const GemmParams& p,
@@ -157,6 +158,10 @@ bool make_adapt(GemmAdapt* g, const AdaptOperands* o, long x_rows, const GemmPar
   g->list = o->list;
   g->cap = o->cap;
   g->rblocks = o->rblocks;
+  g->all = o->all;
+  if (o->all > 0 && !make_tmap(&g->cat, o->cat, static_cast<uint64_t>(p.Nout),
+                               static_cast<uint64_t>(o->n) * adapt_cat_rank(o->rank), w_box))
+    return false;
   return make_tmap(&g->v, o->v, static_cast<uint64_t>(x_rows),
                    static_cast<uint64_t>(o->cap) * o->rblocks * 64, x_box) &&
          make_tmap(&g->b, o->b, static_cast<uint64_t>(o->n) * p.Nout, static_cast<uint64_t>(o->rank), w_box);
@@ -1011,7 +1016,7 @@ moe_status_t check_adapters(const moe_config_t& c, const moe_adapters_t* ad, con
 
 // Workspace of the adapted projections, for either of the two (both widths).
 struct AdaptLayout {
-  size_t v, V, count, list, bad, total;
+  size_t v, V, count, list, bad, cat, total;
 };
 AdaptLayout adapt_layout(const moe_config_t& c, const moe_adapters_t& ad) {
   AdaptLayout L{};
@@ -1028,6 +1033,8 @@ AdaptLayout adapt_layout(const moe_config_t& c, const moe_adapters_t& ad) {
   L.list = take((T + kAdMaxChunk + T / 4 + 4) * 4);
   static_assert(kAdSlices == 8, "one 64-bit word an adapter");
   L.bad = take(n * 8);
+  const size_t cols = n * adapt_cat_rank(ad.rank);
+  L.cat = take(cols <= kAdCatCols ? std::max(c.d_model, c.d_latent) * cols * 2 : 0);
   L.total = o;
   return L;
 }
@@ -1066,6 +1073,12 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
   ops.rank = rank;
   ops.cap = std::min(n, std::min(CH, T));
   ops.rblocks = cdiv(rank, 64);
+  // Few columns over all adapters: lay them side by side for the tiles that use more blocks than that.
+  const long cols = static_cast<long>(n) * adapt_cat_rank(rank);
+  const int all = cdiv(cols, 64);
+  const bool cat = cols <= kAdCatCols && n > 1 && all <= ops.cap * ops.rblocks;
+  ops.all = cat ? all : 0;
+  ops.cat = cat ? at<void>(workspace, L.cat) : nullptr;
   const int chunks = cdiv(T, kAdChunk), splits = std::min(adapter_splits(chunks), K / 64);
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
@@ -1079,15 +1092,17 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
     return MOE_ERR_CUDA;
   auto before = [&] {
     unsigned long long* bad = at<unsigned long long>(workspace, L.bad);
-    launch_k(adapter_check_kernel, n * kAdSlices, 256, 0, st, which, T, static_cast<const uint16_t*>(b),
-             static_cast<long>(p.Nout) * rank, reinterpret_cast<uint8_t*>(bad));
+    launch_k(cat ? adapter_check_kernel<true> : adapter_check_kernel<false>, n * kAdSlices, 256, 0, st, which, T,
+             static_cast<const uint16_t*>(b), static_cast<long>(p.Nout) * rank, reinterpret_cast<uint8_t*>(bad),
+             rank, static_cast<int>(cols),
+             const_cast<uint16_t*>(static_cast<const uint16_t*>(ops.cat)));
     launch_k(adapter_shrink_kernel, dim3(chunks, splits), kGemmThreads, kAdSmem, st, tx, ta, T, K, which, n,
              rank, v);
     // rows a CTA writes: few, so that small batches use many CTAs; more at prefill, where finding the tile's
     // adapters is what a CTA spends its time on
     const int per = T >= 4096 ? 32 : 8;
     launch_k(adapter_pack_kernel, cdiv(T, CH) * cdiv(std::min(T, CH), per), kAdMaxChunk, 0, st, v, splits, T,
-             which, n, rank, ad.scale, bad, CH, ops.cap, ops.rblocks, per, at<int>(workspace, L.count),
+             which, n, rank, ad.scale, bad, CH, ops.cap, ops.rblocks, per, ops.all, at<int>(workspace, L.count),
              at<int>(workspace, L.list), at<uint16_t>(workspace, L.V));
     last_launch(3);
   };

@@ -335,10 +335,12 @@ MOE_API moe_status_t moe_layer_forward_taps(const moe_config_t* cfg, const moe_w
  *   - token_adapter: [T] int32, aligned to 4 bytes (a slice of a longer array may be passed).  An index
  *     outside [-1, n_adapters) latches MOE_ERR_DEVICE_CHECK and means none.
  *   - Adapter weights must be finite.  One adapter's non-finite values never reach another's tokens:
- *     with more than 64 tokens an adapter whose B holds one is left out (its tokens get the projection
- *     alone) and MOE_ERR_DEVICE_CHECK is latched; otherwise they reach its own tokens' outputs.
+ *     in batches whose reduction is not split an adapter whose B holds one is left out (its tokens get
+ *     the projection alone) and MOE_ERR_DEVICE_CHECK is latched; otherwise they reach its own tokens'
+ *     outputs.
  *   - workspace: moe_adapters_workspace_size bytes (host arithmetic; grows with T * min(n_adapters,
- *     256) * 128 bytes), contents need not be initialised.  Calls that share it must not overlap.
+ *     256) * 128 bytes, and by at most 2 KB per feature for copies of B), contents need not be
+ *     initialised.  Calls that share it must not overlap.
  *   - Outputs must not alias inputs.  Errors as for moe_latent_down / moe_latent_up, and
  *     MOE_ERR_UNSUPPORTED for a rank that is no multiple of 8 or above MOE_ADAPTER_MAX_RANK, or for
  *     more adapters than 2^31 rows of their stacked matrices. */

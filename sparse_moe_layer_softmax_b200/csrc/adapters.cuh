@@ -5,15 +5,16 @@
 // adds B_a v_t:
 //   - Up to 64 rows (a decode batch) the weight stream of W sets the time.  The inner products run in
 //     their own small kernel, one CTA per (adapter, range of the reduction), while the projection
-//     kernel already streams W; its finishing warps add B_a v_t in fp32 on the CUDA cores, before the
-//     tile's sum is there (gemm_splitk.cuh).  Every token reads its own adapter only.
+//     kernel already streams W; eight of its warps compute B_a v_t on the tensor cores, v as hi + lo
+//     bf16, adapter by adapter, before the tile's sum is there (gemm_splitk.cuh).
 //   - Larger batches put B_a v_t on the tensor cores: the projection GEMM's reduction is extended, tile
 //     by tile, by one 64-wide k-block per adapter that the tile's rows use.  The activation operand of
 //     that block is v_t for the rows of that adapter and zero for the others, the weight operand the
 //     tile's rows of B_a (TMA fills the columns past the rank with zeros).  A tile of one prompt pays
 //     64 columns on top of the 8192 of the Muse projection, under 1%; nothing is sorted or gathered.
-//     v is rounded to bf16 there (an MMA operand): its error is 2^-9 of the adapter's term, below the
-//     2^-9 of the whole that storing the result costs.
+//     A tile of many adapters of small rank takes their matrices side by side instead (kAdCatCols).
+//     v is rounded to bf16 there (an MMA operand): an error of at most 2^-8 of each product of the
+//     adapter's term, beside the 2^-8 of the whole that storing the result costs.
 //     An MMA multiplies zero rows too, and zero times infinity is NaN: so that one adapter's broken
 //     weights cannot reach the tokens of others, each used B is looked through once per call, and an
 //     adapter that holds a non-finite value is left out and reported.

@@ -331,6 +331,15 @@ def moe_layer_forward_taps(cfg, weights: Weights, u, r, out, taps: dict, logits_
         _stream(stream)))
 
 
+def _on_current_device(*tensors) -> None:
+    """The kernels run on the current device: tensors (not bare addresses) have to live there."""
+    import torch
+    for t in tensors:
+        if t is not None and not isinstance(t, int) and \
+                not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+            raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
+
+
 def make_adapters(a: dict) -> Adapters:
     """moe_adapters_t from a dict of CUDA tensors: scale [n] fp32 and, for the projections it is
     used with, down_a [n, r, d_model], down_b [n, d_latent, r], up_a [n, r, d_latent],
@@ -386,6 +395,7 @@ def moe_latent_down_adapters(cfg, u, p_down, adapters, token_adapter, z_raw, wor
     """z_raw = u P_down^T plus each token's adapter (``adapters`` from make_adapters,
     ``token_adapter`` [T] int32, -1: none)."""
     _check_adapter_shapes(cfg, adapters, token_adapter, ("down",))
+    _on_current_device(u, z_raw, token_adapter)
     workspace_bytes = workspace_bytes or workspace.numel() * workspace.element_size()
     _check("moe_latent_down_adapters", lib().moe_latent_down_adapters(
         ctypes.byref(cfg), _ptr(u), _ptr(p_down), ctypes.byref(adapters), _ptr(token_adapter),
@@ -396,6 +406,7 @@ def moe_latent_up_adapters(cfg, y, p_up, adapters, token_adapter, r, resid_g, ou
                            workspace_bytes=0, stream=None):
     """out = residual update of y P_up^T plus each token's adapter."""
     _check_adapter_shapes(cfg, adapters, token_adapter, ("up",))
+    _on_current_device(y, out, token_adapter)
     workspace_bytes = workspace_bytes or workspace.numel() * workspace.element_size()
     _check("moe_latent_up_adapters", lib().moe_latent_up_adapters(
         ctypes.byref(cfg), _ptr(y), _ptr(p_up), ctypes.byref(adapters), _ptr(token_adapter), _ptr(r),
@@ -410,6 +421,7 @@ def moe_layer_forward_adapters(cfg, weights: Weights, adapters, token_adapter, u
     if workspace is not None and not workspace_bytes:
         workspace_bytes = workspace.numel() * workspace.element_size()
     _check_adapter_shapes(cfg, adapters, token_adapter, ("down", "up"))
+    _on_current_device(u, out, token_adapter)
     _check("moe_layer_forward_adapters", lib().moe_layer_forward_adapters(
         ctypes.byref(cfg), ctypes.byref(weights), ctypes.byref(adapters), _ptr(token_adapter), _ptr(u),
         _ptr(r), _ptr(out), _ptr(logits_out), _ptr(topk_idx_out), _ptr(topk_w_out), _ptr(workspace),
@@ -433,6 +445,8 @@ def moe_layer_forward_few(cfg, weights: Weights, u, r, out, logits_out=None, top
         workspace_bytes = workspace.numel() * workspace.element_size()
     if adapters is not None:
         _check_adapter_shapes(cfg, adapters, token_adapter, ("down", "up"))
+        _on_current_device(token_adapter)
+    _on_current_device(u, out)
     _check("moe_layer_forward_few", lib().moe_layer_forward_few(
         ctypes.byref(cfg), ctypes.byref(weights),
         ctypes.byref(adapters) if adapters is not None else None, _ptr(token_adapter), _ptr(u),

@@ -53,6 +53,27 @@ DeviceInfo& device_info() {
   return d;
 }
 
+// Dynamic shared memory of one kernel, allowed once on each device (the attribute belongs to the device
+// that is current when it is set).
+class SmemLimit {
+ public:
+  bool set(const void* kern, int bytes) {
+    int dev = 0;
+    cudaGetDevice(&dev);
+    const unsigned long long bit = 1ull << (dev & 63);
+    if (done_.load(std::memory_order_acquire) & bit) return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+      cudaGetLastError();
+      return false;
+    }
+    done_.fetch_or(bit, std::memory_order_release);
+    return true;
+  }
+
+ private:
+  std::atomic<unsigned long long> done_{0};
+};
+
 PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
   static std::once_flag once;
@@ -175,12 +196,8 @@ moe_status_t launch_gemm(const void* X, long x_rows, const void* W, long w_rows,
   constexpr int smem = gemm_smem_bytes<kSwap, BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
   auto kern = gemm_tc_kernel<kSwap, BN, kEpi, kStages, Adapt>;
-  static std::once_flag once;  // the attribute is per function; set it once per process
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(kern), smem)) return MOE_ERR_CUDA;
   CUtensorMap tx, tw;
   // X is [x_rows, K], or [x_rows, x_k_period] when its k coordinate wraps (W then has K columns)
   const uint64_t x_cols = static_cast<uint64_t>(p.x_k_period > 0 ? p.x_k_period : p.K);
@@ -214,12 +231,8 @@ moe_status_t launch_gemm_pair(const void* X, long x_rows, const void* W, long w_
   constexpr int smem = gemm_pair_smem_bytes<BN, kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
   auto kern = gemm_tc_pair_kernel<BN, kEpi, kStages, Adapt>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(kern), smem)) return MOE_ERR_CUDA;
   CUtensorMap tx, tw;
   if (p.x_k_period > 0) return MOE_ERR_UNSUPPORTED;  // the pair kernel has no wrapping X
   if (!make_tmap(&tx, X, static_cast<uint64_t>(x_rows), static_cast<uint64_t>(p.K), 128))
@@ -249,12 +262,8 @@ moe_status_t launch_gemm_swap_pair(const void* X, long x_rows, const void* W, lo
   constexpr int smem = gemm_swap_pair_smem_bytes<kEpi, kStages>();
   static_assert(smem <= 232448, "shared memory budget");
   auto kern = gemm_swap_pair_kernel<kEpi, kStages>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(kern), smem)) return MOE_ERR_CUDA;
   if (p.x_k_period > 0 || !p.seg) return MOE_ERR_UNSUPPORTED;
   CUtensorMap tx, tw;
   if (!make_tmap(&tx, X, static_cast<uint64_t>(x_rows), static_cast<uint64_t>(p.K), 128))
@@ -542,12 +551,8 @@ moe_status_t launch_gemm_splitk(const void* X, long x_rows, const void* W, long 
   static_assert(most <= 232448, "shared memory budget");
   const int smem = split_smem(ad);
   auto kern = gemm_splitk_cluster_kernel<kEpi, Adapt>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(kern), most)) return MOE_ERR_CUDA;
   if (x_rows > kSplitBN || splits < 2 || splits > kSplitMaxCluster || p.Nout % 128 ||
       (p.K / 64) % splits)
     return MOE_ERR_UNSUPPORTED;
@@ -593,13 +598,8 @@ moe_status_t do_route(const moe_config_t& c, const void* u, const void* w_router
   float* lbuf = logits ? logits : logits_scratch;
   const size_t small_smem = static_cast<size_t>(kRouterTok) * c.d_model * 2;
   if (c.T <= kSmallRouterMaxT && lbuf && small_smem <= 200 * 1024) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-      attr = cudaFuncSetAttribute(router_logits_small_kernel,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, 200 * 1024);
-    });
-    if (attr != cudaSuccess) return MOE_ERR_CUDA;
+    static SmemLimit limit;
+    if (!limit.set(reinterpret_cast<const void*>(router_logits_small_kernel), 200 * 1024)) return MOE_ERR_CUDA;
     dim3 grid(cdiv(c.n_experts, kRouterExp), cdiv(c.T, kRouterTok));
     launch_k(router_logits_small_kernel, grid, kRouterThreads, small_smem, st,
         static_cast<const uint16_t*>(u), static_cast<const uint16_t*>(w_router), bias, c.T,
@@ -834,13 +834,8 @@ moe_status_t do_combine(const moe_config_t& c, const void* s, const int32_t* inv
     const int nst = std::min(8, (kBulkCombineSmem - 128 - 16 * 8) / B.bytes);
     if (nst >= 2) {
       const size_t smem = 128 + static_cast<size_t>(nst) * B.bytes + 16 * static_cast<size_t>(nst);
-      static std::once_flag once;
-      static cudaError_t attr = cudaSuccess;
-      std::call_once(once, [] {
-        attr = cudaFuncSetAttribute(combine_bf16_bulk_kernel,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, kBulkCombineSmem);
-      });
-      if (attr != cudaSuccess) return MOE_ERR_CUDA;
+      static SmemLimit limit;
+      if (!limit.set(reinterpret_cast<const void*>(combine_bf16_bulk_kernel), kBulkCombineSmem)) return MOE_ERR_CUDA;
       const int grid = std::min(c.T, std::max(device_info().sms, 1));
       launch_k(combine_bf16_bulk_kernel, grid, kBulkCombineConsumers + 32, smem, st,
           sp, E, c.top_k, inv, w, row_ss, parts_b, c.expert_norm, c.eps, yp, c.T, nst);
@@ -1080,12 +1075,8 @@ moe_status_t adapted_projection(const moe_config_t& c, const void* x, const void
   ops.all = cat ? all : 0;
   ops.cat = cat ? at<void>(workspace, L.cat) : nullptr;
   const int chunks = cdiv(T, kAdChunk), splits = std::min(adapter_splits(chunks), K / 64);
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(adapter_shrink_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kAdSmem);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(adapter_shrink_kernel), kAdSmem)) return MOE_ERR_CUDA;
   CUtensorMap tx, ta;
   if (!make_tmap(&tx, x, static_cast<uint64_t>(T), static_cast<uint64_t>(K), kAdChunk) ||
       !make_tmap(&ta, a, static_cast<uint64_t>(n) * rank, static_cast<uint64_t>(K), static_cast<uint32_t>(rank)))
@@ -1221,12 +1212,8 @@ moe_status_t launch_few(const FewParams& p, int smem, cudaStream_t st) {
               make_few_map(&m.ad_up, p.up_a, kF32, R, 1, L, false);
   if (!ok) return MOE_ERR_CUDA;
   auto kern = few_layer_kernel<kF32>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kFewSmem);
-  });
-  if (attr_err != cudaSuccess) return MOE_ERR_CUDA;
+  static SmemLimit limit;
+  if (!limit.set(reinterpret_cast<const void*>(kern), kFewSmem)) return MOE_ERR_CUDA;
   const int sms = device_info().sms;
   if (sms <= 0) return MOE_ERR_CUDA;
   launch_k(few_init_kernel, 1, 128, 0, st, p.bar);

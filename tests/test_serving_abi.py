@@ -159,3 +159,22 @@ def test_make_adapters_checks_shapes():
     for args in ((muse(T=3, d_model=128, d_latent=128), which), (cfg, which.long()), (cfg, which[:2]), (cfg, None)):
         with pytest.raises(ValueError):
             moe._check_adapter_shapes(args[0], ad, args[1], ("down",))
+
+
+def test_tensors_off_the_current_device_are_refused():
+    torch = pytest.importorskip("torch")
+    bf = torch.bfloat16
+    ad = moe.make_adapters({"scale": torch.ones(2), "down_a": torch.zeros(2, 8, 64, dtype=bf),
+                            "down_b": torch.zeros(2, 128, 8, dtype=bf), "up_a": torch.zeros(2, 8, 128, dtype=bf),
+                            "up_b": torch.zeros(2, 64, 8, dtype=bf)})
+    cfg = muse(T=3, d_model=64, d_latent=128)
+    which, u, z = torch.zeros(3, dtype=torch.int32), torch.zeros(3, 64, dtype=bf), torch.zeros(3, 128, dtype=bf)
+    ws = torch.zeros(16, dtype=torch.uint8)
+    for call in (lambda: moe.moe_latent_down_adapters(cfg, u, A, ad, which, z, ws),
+                 lambda: moe.moe_latent_up_adapters(cfg, z, A, ad, which, A, A, u, ws),
+                 lambda: moe.moe_layer_forward_adapters(cfg, weights(), ad, which, u, u, u, workspace=ws),
+                 lambda: moe.moe_layer_forward_few(cfg, weights(), u, u, u, workspace=ws),
+                 lambda: moe.moe_layer_forward_few(cfg, weights(), A, A, A, workspace=A, workspace_bytes=1,
+                                                   adapters=ad, token_adapter=which)):
+        with pytest.raises(ValueError, match="current CUDA device"):
+            call()

@@ -367,7 +367,7 @@ MOE_API moe_status_t moe_layer_forward_adapters(const moe_config_t* cfg, const m
                                                 void* workspace, size_t workspace_bytes, void* stream);
 
 /* The whole layer, as moe_layer_forward defines it, for 1 .. MOE_FEW_MAX_TOKENS tokens in one
- * persistent kernel (and one memset of its barrier counters): single-stream decoding, or the
+ * persistent kernel (and a small one that zeroes its barrier counters): single-stream decoding, or the
  * verification of a few drafted tokens, where the launches of the batch path cost as much as the
  * weights.  bf16 or fp32, every gate, norm and residual mode of moe_layer_forward.
  *   - adapters (optional, bf16 with latent projections): both projections get each token's adapter,

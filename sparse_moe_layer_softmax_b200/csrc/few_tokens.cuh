@@ -733,11 +733,11 @@ __global__ void few_init_kernel(unsigned* bar) {
 
 // The layer.  Grid: one CTA per SM, cooperative (every CTA resident).  Warps 0-7 multiply: chunk c of
 // the CTA's stream (one ring stage) belongs to warp c % W (W <= 8), so W stages are in work at once and
-// a tile's chunks meet as up to W partial tiles in shared memory.  The ring holds a multiple
-// of W stages: then one warp alone waits on a stage's barrier, phase after phase (with another number
-// a warp could come to a stage whose previous fill has not landed, and take its parity for its own).  Warps 8-10 add the partial tiles
-// in chunk order and finish the tile (one barrier per tile among all warps had kept the stream at half
-// its rate).  Warp 11 is the producer.
+// a tile's chunks meet as up to W partial tiles in shared memory.  The ring holds a multiple of W stages:
+// then one warp alone waits on a stage's barrier, phase after phase (with another number a warp could
+// come to a stage whose previous fill has not landed, and take its parity for its own).  Warps 8-10 add
+// the partial tiles in chunk order and finish the tile (one barrier per tile among all warps had kept the
+// stream at half its rate).  Warp 11 is the producer.
 template <bool kF32>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_layer_kernel(const __grid_constant__ FewParams p, const __grid_constant__ FewMaps maps) {

@@ -86,9 +86,10 @@ constexpr int split_adapt_smem(int rank) {
 // in kSplitAdaptThreads threads while the tile's weights stream in, and behind that stream every load
 // takes about 3 us: what counts is how few of them wait for one another.  So the rows are grouped by
 // adapter, the adapters' B rows come in as one bulk copy each (a part of B is contiguous), as many as
-// half a buffer holds while the other half is in use, and v's partial sums as one batch of loads; then m16n8k16 products put 16 features on M,
-// eight of an adapter's rows on N and the rank on K.  (Loading B into fragments adapter by adapter, 64
-// adapters of rank 16 took 60 us; a thread to 8 features on the CUDA cores, 12 of rank 64 also 60.)
+// half a buffer holds while the other half is in use, and v's partial sums as one batch of loads; then
+// m16n8k16 products put 16 features on M, eight of an adapter's rows on N and the rank on K.  (Loading B
+// into fragments adapter by adapter, 64 adapters of rank 16 took 60 us; a thread to 8 features on the
+// CUDA cores, 12 of rank 64 also 60.)
 // v enters as hi + lo, so the term keeps fp32's accuracy to 2^-17.
 template <int NS>
 __device__ __forceinline__ void splitk_adapt(const SplitAdapt& ad, const GemmParams& p, uint32_t rank,

@@ -333,10 +333,15 @@ def moe_layer_forward_taps(cfg, weights: Weights, u, r, out, taps: dict, logits_
 
 def _on_current_device(*tensors) -> None:
     """The kernels run on the current device: tensors (not bare addresses) have to live there."""
-    import torch
+    current = None
     for t in tensors:
-        if t is not None and not isinstance(t, int) and \
-                not (t.is_cuda and t.get_device() == torch.cuda.current_device()):
+        if t is None or isinstance(t, int):
+            continue
+        at = t.get_device()  # negative: not a CUDA tensor
+        if current is None and at >= 0:
+            import torch
+            current = torch.cuda.current_device()
+        if at < 0 or at != current:
             raise ValueError(f"a tensor on {t.device}, which is not the current CUDA device")
 
 
@@ -353,33 +358,34 @@ def make_adapters(a: dict) -> Adapters:
         if t is None:
             continue
         if t.dtype != torch.bfloat16 or t.dim() != 3 or not t.is_contiguous() or t.shape[0] != n or \
-                rank not in (None, t.shape[axis]):
+                rank not in (None, t.shape[axis]) or t.device != a["scale"].device:
             raise ValueError(f"make_adapters: {name} is a contiguous bf16 tensor of {n} adapters "
-                             "of one rank")
+                             "of one rank, on the device of scale")
         rank = t.shape[axis]
     if rank is None:
         raise ValueError("make_adapters: no adapter weights")
     ad = Adapters(n_adapters=n, rank=rank, **{k: _ptr(a.get(k)) for k, _ in Adapters._fields_[2:]})
     ad.tensors = dict(a)
+    ad.index_dtype, ad.device_index = torch.int32, a["scale"].get_device()
+    size = lambda name, axis: None if a.get(name) is None else a[name].shape[axis]
+    ad.widths = {"down": (size("down_a", 2), size("down_b", 1)), "up": (size("up_a", 2), size("up_b", 1))}
     return ad
 
 
 def _check_adapter_shapes(cfg, adapters, token_adapter, pairs):
-    """The tensors that ``make_adapters`` kept, and the token map, against a configuration."""
-    import torch
-    if token_adapter is None or token_adapter.dtype != torch.int32 or \
-            token_adapter.numel() != cfg.T or not token_adapter.is_contiguous():
+    """The widths that ``make_adapters`` noted, and the token map, against a configuration.  (A decode
+    step's kernels take as long as its call: whole numbers are compared, no shapes or device objects.)"""
+    t = token_adapter
+    if t is None or t.dtype != adapters.index_dtype or t.numel() != cfg.T or not t.is_contiguous():
         raise ValueError("token_adapter: a contiguous int32 tensor with one entry per token")
-    if token_adapter.device != adapters.tensors["scale"].device:
+    if t.get_device() != adapters.device_index:
         raise ValueError("token_adapter and the adapters are on different devices")
-    for name, t in adapters.tensors.items():
-        if name.rsplit("_", 1)[0] not in pairs or t is None:
-            continue
-        want = {"down_a": (2, cfg.d_model), "down_b": (1, cfg.d_latent), "up_a": (2, cfg.d_latent),
-                "up_b": (1, cfg.d_model)}[name]
-        if t.shape[want[0]] != want[1]:
-            raise ValueError(f"adapters: {name} has {t.shape[want[0]]} values where the layer has "
-                             f"{want[1]}")
+    d, L = cfg.d_model, cfg.d_latent
+    for pair in pairs:
+        a, b = (d, L) if pair == "down" else (L, d)
+        for name, have, want in zip(("a", "b"), adapters.widths[pair], (a, b)):
+            if have not in (None, want):
+                raise ValueError(f"adapters: {pair}_{name} has {have} values where the layer has {want}")
 
 
 def adapters_workspace_size(cfg: Config, adapters: Adapters) -> int:
